@@ -606,6 +606,213 @@ CSA_API csa_status csa_block_sparse_prefill(const void* Q, const void* K, const 
                                     int S, int Hq, int Hkv, int D, int tile_m, int L,
                                     float scale, void* O, csa_stream stream);
 
+/* ---------------------------------------------------------------- rotary positions
+ * The full form of csa_rope for a serving or training loop (no counterpart in
+ * the pages beyond RoPE itself): both pair layouts, part of the head, scaled
+ * frequencies, a position per token, strided views, the gradient.
+ *
+ * csa_rotary_table: the rot/2 frequencies as 64-bit fractions of a turn per
+ * position (w / 2 pi * 2^64, whole turns dropped), for csa_rotary.  With
+ * w_i = theta^(-2i/rot), f = factor:
+ *   CSA_ROTARY_NONE    w_i
+ *   CSA_ROTARY_LINEAR  w_i / f  (position interpolation)
+ *   CSA_ROTARY_NTK     (theta f^(rot/(rot-2)))^(-2i/rot)
+ *   CSA_ROTARY_TURNS   (1 - g) w_i / f + g w_i,  g = clamp((r_i - low) /
+ *                      (high - low), 0, 1),  r_i = orig_len w_i / 2 pi: the
+ *                      pair's turns over the original length
+ *   CSA_ROTARY_RAMP    the same blend with g = 1 - clamp((i - lo) / max(hi -
+ *                      lo, 0.001), 0, 1), lo = max(0, floor(d(high))), hi =
+ *                      min(rot - 1, ceil(d(low))), d(t) = rot ln(orig_len /
+ *                      (2 pi t)) / (2 ln theta): the ramp over the pair index
+ * `freqs` (device, rot/2 doubles, radians per position) replaces the formula
+ * when not NULL; the other numbers are then not used.
+ *   rot even, 2 <= rot <= 512;  theta > 1;  factor >= 1;  orig_len >= 1 and
+ *   0 < low < high where they are used.  table: rot/2 uint64 (output). */
+typedef enum csa_rotary_scaling {
+  CSA_ROTARY_NONE = 0,
+  CSA_ROTARY_LINEAR = 1,
+  CSA_ROTARY_NTK = 2,
+  CSA_ROTARY_TURNS = 3,
+  CSA_ROTARY_RAMP = 4
+} csa_rotary_scaling;
+
+CSA_API csa_status csa_rotary_table(int rot, double theta, int scaling, double factor,
+                                    double orig_len, double low, double high, const double* freqs,
+                                    uint64_t* table, csa_stream stream);
+
+/* csa_rotary: y = rotation of x for one or two tensors (queries and keys) in
+ * one launch.  Token (b, s) sits at p = positions[b * pos_stride_b + s], or
+ * pos0 + s when positions is NULL; with t = p w_i, for i < rot/2,
+ *   y_a = A (x_a cos t - x_c sin t),  y_c = A (x_c cos t + x_a sin t),
+ *   (a, c) = (i, i + rot/2) for CSA_ROTARY_HALF, (2i, 2i + 1) for
+ *   CSA_ROTARY_INTERLEAVED, A = amplitude;
+ * values from rot on are copied.  transpose != 0 turns by -t (same A): the
+ * gradient of x from that of y.  The angle is p w_i modulo one turn in 64-bit
+ * integers, so far positions keep their accuracy; sums are fp32.
+ *   x, y [B, S, H, D] of `dtype` by strides in elements (batch, token, head;
+ *   the last index dense).  y == x with equal strides turns in place; other
+ *   overlaps are not allowed.  H2 = 0: no second tensor.  x and y need only
+ *   their element's alignment (CSA_ROTARY_INTERLEAVED: two elements').
+ *   D even, D <= 512;  rot even, 2 <= rot <= D;  strides non-negative, and even for
+ *   CSA_ROTARY_INTERLEAVED, y's not below D (distinct rows);  B * S * D <= 2^29;
+ *   any int32 position. */
+typedef enum csa_rotary_layout { CSA_ROTARY_HALF = 0, CSA_ROTARY_INTERLEAVED = 1 } csa_rotary_layout;
+
+typedef struct csa_rotary_desc {
+  const void* x;
+  void* y;
+  int H;
+  int64_t x_stride[3], y_stride[3]; /* batch, token, head */
+  const void* x2;
+  void* y2;
+  int H2;
+  int64_t x2_stride[3], y2_stride[3];
+  csa_dtype dtype;
+  int B;
+  int64_t S;
+  int D, rot;
+  int layout; /* csa_rotary_layout */
+  int transpose;
+  const uint64_t* table;    /* [rot/2], csa_rotary_table */
+  float amplitude;
+  const int32_t* positions; /* NULL or device */
+  int64_t pos_stride_b;
+  int64_t pos0;
+} csa_rotary_desc;
+
+CSA_API csa_status csa_rotary(const csa_rotary_desc* d, csa_stream stream);
+
+/* ---------------------------------------------------------------- bounded cache
+ * A KV cache of at most `budget` slots per sequence whose tokens are kept by
+ * the attention weight they have received (csa_prefix_decode adds it up), in
+ * the manner of the importance-based compression of the Token Sparse summary
+ * (section 2) carried over to decoding.  Slots are in no order: attention
+ * does not depend on it (keys are rotated already), and `positions` says
+ * where each slot's token stands.
+ *   K, V       [B, Hkv, T, D] of `dtype` by strides in elements (sequence,
+ *              head, slot; last index dense; slots must not overlap; these and
+ *              the rows copied into them need only their element's alignment)
+ *   weights    [B, Hkv, T] fp32, positions [B, Hkv, T] int32 (dense)
+ *   len        [B] int32: slots in use, 0 .. budget; slots behind stay as they are
+ *   next_pos   [B] int32: the next token's position; < 0: the sequence is
+ *              inactive and csa_cache_insert leaves it alone
+ *   budget <= T < 2^31;  n_sink, n_local >= 0
+ * Protected slots: position < n_sink, or >= next_pos - n_local.  The others
+ * rank by weight (NaN counts as -infinity; -0 == +0), equal weights by slot.
+ *   D <= 1024;  B * Hkv <= 65535. */
+typedef struct csa_cache_desc {
+  void* K;
+  void* V;
+  csa_dtype dtype;
+  int B, Hkv, D;
+  int64_t T;
+  int64_t k_stride[3], v_stride[3];
+  float* weights;
+  int32_t* positions;
+  int32_t* len;
+  int32_t* next_pos;
+  int64_t budget;
+  int n_sink, n_local;
+  int32_t* counters; /* [B], zeroed once; each call leaves it zero */
+} csa_cache_desc;
+
+/* csa_cache_insert: one new token per active sequence (k, v [B, Hkv, D] by
+ * strides (sequence, head), last index dense) goes into slot len[b] while
+ * len[b] < budget, else over the unprotected slot of least weight (each head
+ * its own; the lowest slot among equals).  The slot gets weight 0 and
+ * position next_pos[b]; then len[b] (up to budget) and next_pos[b] advance by
+ * one.  Needs n_sink + n_local < budget.  A length outside [0, budget], or no
+ * unprotected slot (positions that are not distinct), records
+ * CSA_ERR_DEVICE_INDEX and leaves that sequence's (that head's) slots alone.
+ * Calls that share a cache or its counters must not overlap on the GPU. */
+CSA_API csa_status csa_cache_insert(const csa_cache_desc* c, const void* k,
+                                    const int64_t* k_stride, const void* v,
+                                    const int64_t* v_stride, csa_stream stream);
+
+/* csa_cache_compress: the rows of a longer cache or prompt into cache `c`.  Of
+ * the first n = src_len[b] rows (NULL: S) of each (sequence, head) all are
+ * kept when n <= budget, else the protected ones and the heaviest others up to
+ * `budget` (the lower row among equals; of more protected rows than fit, the
+ * lowest), and copied in row order to slots 0 ..  with their weights and
+ * positions; len[b] = the rows kept; c->next_pos (NULL: not written) = the
+ * next position.
+ *   src K, V by strides (sequence, head, row); weights [B, Hkv, S] fp32;
+ *   positions NULL (the row number) or [B, Hkv, S] int32; src_next_pos NULL
+ *   (n) or [B], required with positions.  n_sink + n_local <= budget.
+ *   Source and cache must not overlap.  S < 2^31; c->counters is not used. */
+typedef struct csa_cache_source {
+  const void* K;
+  const void* V;
+  int64_t S;
+  int64_t k_stride[3], v_stride[3];
+  const float* weights;
+  const int32_t* positions;
+  const int32_t* len;
+  const int32_t* next_pos;
+} csa_cache_source;
+
+CSA_API csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* src,
+                                      csa_stream stream);
+
+/* ---------------------------------------------------------------- shared prefixes
+ * csa_prefix_decode: one decode token per sequence over a prefix that several
+ * sequences share and over each sequence's own cache, in one softmax (exact
+ * split-K attention as in a5 / a6, each prefix read once for all its
+ * sequences):
+ *   s_gj = scale q[b, h*G+g] . k_j over prefix rows [0, prefix_len[n]) of the
+ *          sequence's group n and own slots [0, len[b]),  G = Hq/Hkv
+ *   lse  = log sum_j exp(s_gj);  out = sum_j exp(s_gj - lse) v_j
+ *   weights[b, h, j] = decay weights[b, h, j] + sum_g exp(s_gj - lse_g) for the
+ *          own slots j < len[b] (decay 0: the old value is not read)
+ * A row with no key gets out = 0, lse = -inf.  K and V rows past the lengths
+ * are never used, whatever they hold.
+ *   q [B, Hq, D] dense;  out [B, Hq, D] of out_dtype;  lse_out NULL or [B, Hq]
+ *   fp32;  weights NULL or [B, Hkv, T] fp32
+ *   N prefixes (0: none): Kp, Vp [N, Hkv, Tp, D] by strides (prefix, head,
+ *   token); prefix_len NULL (Tp) or [N] int32;  group_start [N + 1] int32
+ *   ascending: sequences group_start[n] .. group_start[n+1]-1 share prefix n, others
+ *   have none (NULL: N = 1, all sequences)
+ *   K, V [B, Hkv, T, D] by strides (sequence, head, slot), T = 0: none;
+ *   len NULL (T) or [B] int32
+ *   CSA_BF16: bf16 tensor-core products, weights of V rounded to bf16, fp32
+ *   sums and statistics; CSA_F32: fp32 throughout.  D in {64, 128};  G <= 16;
+ *   N <= 64;  strides multiples of 16 bytes;  B * Hkv <= 65535.
+ * A length or group bound out of range records CSA_ERR_DEVICE_INDEX and is clamped.
+ *   workspace >= csa_prefix_decode_workspace_bytes(...) (current device), not
+ *   kept between calls and needing no initial value; calls that share one
+ *   must not overlap on the GPU. */
+typedef struct csa_prefix_decode_desc {
+  csa_dtype dtype;
+  int B, Hq, Hkv, D;
+  float scale;
+  const void* q;
+  int N;
+  int64_t Tp;
+  const void* Kp;
+  const void* Vp;
+  int64_t kp_stride[3], vp_stride[3];
+  const int32_t* prefix_len;
+  const int32_t* group_start;
+  int64_t T;
+  const void* K;
+  const void* V;
+  int64_t k_stride[3], v_stride[3];
+  const int32_t* len;
+  void* out;
+  csa_dtype out_dtype;
+  float* lse_out;
+  float* weights;
+  float decay;
+  void* workspace;
+  int64_t workspace_bytes;
+} csa_prefix_decode_desc;
+
+/* `weights`: whether the calls add up weights.  < 0 on sizes csa_prefix_decode
+ * refuses. */
+CSA_API int64_t csa_prefix_decode_workspace_bytes(csa_dtype dtype, int B, int Hq, int Hkv, int D,
+                                                  int N, int64_t Tp, int64_t T, int weights);
+CSA_API csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

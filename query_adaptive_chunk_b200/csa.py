@@ -36,6 +36,7 @@ if not os.path.exists(LIB_PATH):
 lib = ctypes.CDLL(LIB_PATH)
 
 _vp, _i, _i64, _f, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_uint64
+_d, _st3, _st2 = ctypes.c_double, ctypes.c_int64 * 3, ctypes.c_int64 * 2
 _SIGS = {
     "csa_version": (_i, []),
     "csa_last_error_string": (ctypes.c_char_p, []),
@@ -85,6 +86,12 @@ _SIGS = {
     "csa_lse_merge": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp]),
     "csa_decode_step": (_i, [_vp, _vp]),
     "csa_decode_step_host": (_i, [_vp, _vp, _vp, _vp, _vp]),
+    "csa_rotary_table": (_i, [_i, _d, _i, _d, _d, _d, _d, _vp, _vp, _vp]),
+    "csa_rotary": (_i, [_vp, _vp]),
+    "csa_cache_insert": (_i, [_vp, _vp, _vp, _vp, _vp, _vp]),
+    "csa_cache_compress": (_i, [_vp, _vp, _vp]),
+    "csa_prefix_decode_workspace_bytes": (_i64, [_i, _i, _i, _i, _i, _i, _i64, _i64, _i]),
+    "csa_prefix_decode": (_i, [_vp, _vp]),
     "csa_block_sparse_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                       _vp, _vp]),
 }
@@ -396,3 +403,117 @@ def csa_block_sparse_prefill(Q, K, V, idx, count, kmax, B, S, Hq, Hkv, D, tile_m
                              stream=None):
     _check(lib.csa_block_sparse_prefill(_p(Q), _p(K), _p(V), _p(idx), _p(count), kmax, B, S, Hq,
                                         Hkv, D, tile_m, L, scale, _p(O), _s(stream)))
+
+
+CSA_ROTARY_NONE, CSA_ROTARY_LINEAR, CSA_ROTARY_NTK, CSA_ROTARY_TURNS, CSA_ROTARY_RAMP = range(5)
+CSA_ROTARY_HALF, CSA_ROTARY_INTERLEAVED = 0, 1
+_ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "turns": 3, "ramp": 4}
+_ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
+
+
+def _need(cond, why: str):
+    """The binding's own checks of tensor arguments, reported like the library's."""
+    if not cond:
+        raise CsaError(1, why)
+
+
+class RotaryDesc(ctypes.Structure):
+    """ctypes mirror of csa_rotary_desc."""
+    _fields_ = [
+        ("x", _vp), ("y", _vp), ("H", _i), ("x_stride", _st3), ("y_stride", _st3),
+        ("x2", _vp), ("y2", _vp), ("H2", _i), ("x2_stride", _st3), ("y2_stride", _st3),
+        ("dtype", _i), ("B", _i), ("S", _i64), ("D", _i), ("rot", _i), ("layout", _i),
+        ("transpose", _i), ("table", _vp), ("amplitude", _f), ("positions", _vp),
+        ("pos_stride_b", _i64), ("pos0", _i64),
+    ]
+
+
+class CacheDesc(ctypes.Structure):
+    """ctypes mirror of csa_cache_desc."""
+    _fields_ = [
+        ("K", _vp), ("V", _vp), ("dtype", _i), ("B", _i), ("Hkv", _i), ("D", _i), ("T", _i64),
+        ("k_stride", _st3), ("v_stride", _st3), ("weights", _vp), ("positions", _vp),
+        ("len", _vp), ("next_pos", _vp), ("budget", _i64), ("n_sink", _i), ("n_local", _i),
+        ("counters", _vp),
+    ]
+
+
+class CacheSource(ctypes.Structure):
+    """ctypes mirror of csa_cache_source."""
+    _fields_ = [
+        ("K", _vp), ("V", _vp), ("S", _i64), ("k_stride", _st3), ("v_stride", _st3),
+        ("weights", _vp), ("positions", _vp), ("len", _vp), ("next_pos", _vp),
+    ]
+
+
+class PrefixDecodeDesc(ctypes.Structure):
+    """ctypes mirror of csa_prefix_decode_desc."""
+    _fields_ = [
+        ("dtype", _i), ("B", _i), ("Hq", _i), ("Hkv", _i), ("D", _i), ("scale", _f), ("q", _vp),
+        ("N", _i), ("Tp", _i64), ("Kp", _vp), ("Vp", _vp), ("kp_stride", _st3),
+        ("vp_stride", _st3), ("prefix_len", _vp), ("group_start", _vp), ("T", _i64), ("K", _vp),
+        ("V", _vp), ("k_stride", _st3), ("v_stride", _st3), ("len", _vp), ("out", _vp),
+        ("out_dtype", _i), ("lse_out", _vp), ("weights", _vp), ("decay", _f), ("workspace", _vp),
+        ("workspace_bytes", _i64),
+    ]
+
+
+def _fill(d, kw):
+    """Fields by name: tensors become their data pointers, dtypes their codes,
+    stride sequences C arrays."""
+    for k, v in kw.items():
+        if isinstance(v, torch.Tensor):
+            v = v.data_ptr()
+        elif isinstance(v, torch.dtype):
+            v = _dt(v)
+        elif k.endswith("_stride"):
+            v = _st3(*v)
+        setattr(d, k, v)
+    return d
+
+
+def rotary_desc(**kw) -> RotaryDesc:
+    return _fill(RotaryDesc(), kw)
+
+
+def cache_desc(**kw) -> CacheDesc:
+    return _fill(CacheDesc(), kw)
+
+
+def cache_source(**kw) -> CacheSource:
+    return _fill(CacheSource(), kw)
+
+
+def prefix_decode_desc(**kw) -> PrefixDecodeDesc:
+    return _fill(PrefixDecodeDesc(), kw)
+
+
+def csa_rotary_table(rot, theta, scaling, factor, orig_len, low, high, freqs, table, stream=None):
+    if isinstance(scaling, str):
+        scaling = _ROTARY_SCALING[scaling]
+    _check(lib.csa_rotary_table(rot, theta, scaling, factor, orig_len, low, high, _p(freqs),
+                                _p(table), _s(stream)))
+
+
+def csa_rotary(desc: RotaryDesc, stream=None):
+    _check(lib.csa_rotary(ctypes.byref(desc), _s(stream)))
+
+
+def csa_cache_insert(desc: CacheDesc, k, k_stride, v, v_stride, stream=None):
+    _check(lib.csa_cache_insert(ctypes.byref(desc), _p(k), _st2(*k_stride), _p(v),
+                                _st2(*v_stride), _s(stream)))
+
+
+def csa_cache_compress(desc: CacheDesc, source: CacheSource, stream=None):
+    _check(lib.csa_cache_compress(ctypes.byref(desc), ctypes.byref(source), _s(stream)))
+
+
+def csa_prefix_decode_workspace_bytes(dtype, B, Hq, Hkv, D, N, Tp, T, weights) -> int:
+    n = lib.csa_prefix_decode_workspace_bytes(_dt(dtype), B, Hq, Hkv, D, N, Tp, T, int(weights))
+    if n < 0:
+        raise CsaError(1, csa_last_error_string())
+    return n
+
+
+def csa_prefix_decode(desc: PrefixDecodeDesc, stream=None):
+    _check(lib.csa_prefix_decode(ctypes.byref(desc), _s(stream)))

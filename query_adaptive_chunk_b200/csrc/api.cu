@@ -88,15 +88,16 @@ csa_status launch_ctx(csa_stream stream, csa::Launch* l) {
   return CSA_OK;
 }
 
-// A required device pointer: not NULL, 16-byte aligned, device or managed
-// memory of the current device.
-csa_status check_ptr(const void* p, const char* name, bool required = true) {
+// A required device pointer: not NULL, 16-byte aligned (or as given), device
+// or managed memory of the current device.
+csa_status check_ptr(const void* p, const char* name, bool required = true, int align = 16) {
   if (p == nullptr) {
     if (!required) return CSA_OK;
     return fail(CSA_ERR_INVALID_ARG, std::string(name) + " is NULL");
   }
-  if (reinterpret_cast<uintptr_t>(p) % 16 != 0)
-    return fail(CSA_ERR_INVALID_ARG, std::string(name) + " is not 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(p) % align != 0)
+    return fail(CSA_ERR_INVALID_ARG,
+                std::string(name) + " is not " + std::to_string(align) + "-byte aligned");
   cudaPointerAttributes a;
   cudaError_t e = cudaPointerGetAttributes(&a, p);
   if (e != cudaSuccess) {
@@ -1158,6 +1159,381 @@ csa_status csa_token_decompress(const void* Oc, const int32_t* idx, const int32_
   return finish(csa::launch_tsa_scatter(l, Oc, idx, count, S, B, S, S, Hq, Hkv, D,
                                         static_cast<int32_t*>(scratch), O),
                 "token decompress launch");
+}
+
+}  // extern "C"
+
+
+/* ---- rotary positions, bounded cache, shared prefixes ---- */
+
+namespace {
+
+// Device pointers of the strided calls.  n elements of size es by strides:
+// the byte range [lo, hi) that the tensor covers.
+struct Extent {
+  uintptr_t lo = 0, hi = 0;
+  bool overlaps(const Extent& o) const { return lo < o.hi && o.lo < hi; }
+};
+// Strides must be non-negative and the whole extent below 2^62 bytes.
+bool extent_of(const void* p, const int64_t* n, const int64_t* st, int dims, int64_t last, int es,
+               Extent* x) {
+  __int128 most = last - 1;
+  for (int i = 0; i < dims; ++i) {
+    if (st[i] < 0) return false;
+    if (n[i] > 0) most += static_cast<__int128>(n[i] - 1) * st[i];
+  }
+  if (most >= (static_cast<__int128>(1) << 60)) return false;
+  x->lo = reinterpret_cast<uintptr_t>(p);
+  x->hi = x->lo + static_cast<uintptr_t>(most + 1) * es;
+  return true;
+}
+
+int dtype_size(csa_dtype d) { return d == CSA_BF16 ? 2 : 4; }
+
+csa_status rotary_tensor(const csa_rotary_desc* d, const void* x, void* y, int H, const int64_t* xs,
+                         const int64_t* ys, const char* name, csa::RotaryArgs::Tensor* t) {
+  const std::string nm(name);
+  const int64_t n[3] = {d->B, d->S, H};
+  const int es = dtype_size(d->dtype);
+  Extent ex, ey;
+  CSA_REQUIRE(extent_of(x, n, xs, 3, d->D, es, &ex) && extent_of(y, n, ys, 3, d->D, es, &ey),
+              nm + ": strides must be non-negative");
+  if (d->layout == CSA_ROTARY_INTERLEAVED)
+    for (int i = 0; i < 3; ++i)
+      CSA_SUPPORT(xs[i] % 2 == 0 && ys[i] % 2 == 0, nm + ": interleaved pairs need even strides");
+  for (int i = 0; i < 3; ++i)
+    CSA_REQUIRE(n[i] <= 1 || ys[i] >= d->D, nm + " output: rows overlap (a stride is below D)");
+  const bool same = x == y && xs[0] == ys[0] && xs[1] == ys[1] && xs[2] == ys[2];
+  CSA_TRY(check_ptr(x, name, true, es));
+  CSA_TRY(check_ptr(y, (nm + " output").c_str(), true, es));
+  CSA_REQUIRE(x != y || same, nm + ": in place needs equal strides");
+  t->x = x;
+  t->y = y;
+  t->H = H;
+  for (int i = 0; i < 3; ++i) {
+    t->xst[i] = xs[i];
+    t->yst[i] = ys[i];
+  }
+  return CSA_OK;
+}
+
+csa_status cache_checks(const csa_cache_desc* c, bool insert) {
+  CSA_REQUIRE(c != nullptr, "the cache descriptor is NULL");
+  CSA_REQUIRE(valid_dtype(c->dtype), "dtype");
+  CSA_REQUIRE(c->B >= 0 && c->Hkv > 0 && c->D > 0 && c->T > 0, "B must be non-negative; Hkv, D and T positive");
+  CSA_REQUIRE(c->budget > 0 && c->budget <= c->T, "budget must be in [1, T]");
+  CSA_REQUIRE(c->n_sink >= 0 && c->n_local >= 0, "n_sink and n_local must be non-negative");
+  const int64_t kept = static_cast<int64_t>(c->n_sink) + c->n_local;
+  if (insert)
+    CSA_REQUIRE(kept < c->budget, "n_sink + n_local must be below budget");
+  else
+    CSA_REQUIRE(kept <= c->budget, "n_sink + n_local must not exceed budget");
+  CSA_SUPPORT(c->D <= 1024, "D must be <= 1024");
+  CSA_SUPPORT(c->T < 2147483648LL, "T must be < 2^31");
+  CSA_SUPPORT(static_cast<int64_t>(c->B) * c->Hkv <= 65535, "B*Hkv must be <= 65535");
+  return CSA_OK;
+}
+
+// A strided [B, Hkv, rows, D] tensor, its indices in any order, D dense.
+csa_status kv_extent(const void* p, const int64_t* n, const int64_t* st, int D, int es,
+                     const char* name, Extent* x) {
+  CSA_REQUIRE(extent_of(p, n, st, 3, D, es, x), std::string(name) + ": strides must be non-negative");
+  for (int i = 0; i < 3; ++i)
+    CSA_REQUIRE(n[i] <= 1 || st[i] >= D, std::string(name) + ": rows overlap (a stride is below D)");
+  return CSA_OK;
+}
+
+csa_status cache_ptrs(const csa_cache_desc* c, bool insert, Extent* ek, Extent* ev) {
+  const int es = dtype_size(c->dtype);
+  CSA_TRY(check_ptr(c->K, "K", true, es));
+  CSA_TRY(check_ptr(c->V, "V", true, es));
+  CSA_TRY(check_ptr(c->weights, "weights"));
+  CSA_TRY(check_ptr(c->positions, "positions"));
+  CSA_TRY(check_ptr(c->len, "len"));
+  CSA_TRY(check_ptr(c->next_pos, "next_pos", insert));
+  if (insert) CSA_TRY(check_ptr(c->counters, "counters"));
+  const int64_t n[3] = {c->B, c->Hkv, c->T};
+  CSA_TRY(kv_extent(c->K, n, c->k_stride, c->D, es, "K", ek));
+  CSA_TRY(kv_extent(c->V, n, c->v_stride, c->D, es, "V", ev));
+  return CSA_OK;
+}
+
+csa::CacheArgs cache_args(const csa_cache_desc* c) {
+  csa::CacheArgs a{};
+  a.K = c->K;
+  a.V = c->V;
+  for (int i = 0; i < 3; ++i) {
+    a.kst[i] = c->k_stride[i];
+    a.vst[i] = c->v_stride[i];
+  }
+  a.weights = c->weights;
+  a.positions = c->positions;
+  a.len = c->len;
+  a.next_pos = c->next_pos;
+  a.counters = c->counters;
+  a.bf16 = c->dtype == CSA_BF16;
+  a.B = c->B;
+  a.Hkv = c->Hkv;
+  a.D = c->D;
+  a.budget = static_cast<int>(c->budget);
+  a.n_sink = c->n_sink;
+  a.n_local = c->n_local;
+  a.T = c->T;
+  return a;
+}
+
+csa_status prefix_sizes(csa_dtype dtype, int B, int Hq, int Hkv, int D, int N, int64_t Tp,
+                        int64_t T) {
+  CSA_REQUIRE(valid_dtype(dtype), "dtype");
+  CSA_REQUIRE(B >= 0 && Hq > 0 && Hkv > 0 && N >= 0 && Tp >= 0 && T >= 0,
+              "B, N, Tp, T must be non-negative; Hq, Hkv positive");
+  CSA_REQUIRE(Hq % Hkv == 0, "Hq must be a multiple of Hkv");
+  CSA_SUPPORT(D == 64 || D == 128, "D must be 64 or 128");
+  CSA_SUPPORT(Hq / Hkv <= 16, "Hq/Hkv must be <= 16");
+  CSA_SUPPORT(N <= 64, "N must be <= 64");
+  CSA_SUPPORT(static_cast<int64_t>(B) * Hkv <= 65535, "B*Hkv must be <= 65535");
+  CSA_SUPPORT(Tp < 2147483584LL && T < 2147483584LL, "Tp and T must be < 2^31 - 64");
+  // the chunks of all units are numbered with 32 bits (row tiles of 32 at least)
+  const int64_t chunks = (static_cast<int64_t>(B) * (Hq / Hkv) / 32 + N) * Hkv * ((Tp + 63) / 64) +
+                         static_cast<int64_t>(B) * Hkv * ((T + 63) / 64);
+  CSA_SUPPORT(N == 0 ? static_cast<int64_t>(B) * Hkv * ((T + 63) / 64) < 2147483648LL
+                     : chunks < 2147483648LL,
+              "too many keys in all (chunks of 64 keys per row tile must be < 2^31)");
+  return CSA_OK;
+}
+
+csa_status strides16(const int64_t* st, int es, const char* name) {
+  for (int i = 0; i < 3; ++i) {
+    CSA_REQUIRE(st[i] >= 0, std::string(name) + ": strides must be non-negative");
+    CSA_SUPPORT(st[i] * es % 16 == 0, std::string(name) + ": strides must be multiples of 16 bytes");
+  }
+  return CSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+csa_status csa_rotary_table(int rot, double theta, int scaling, double factor, double orig_len,
+                            double low, double high, const double* freqs, uint64_t* table,
+                            csa_stream stream) {
+  CSA_REQUIRE(rot >= 2 && rot % 2 == 0, "rot must be even and >= 2");
+  CSA_SUPPORT(rot <= 512, "rot must be <= 512");
+  if (freqs == nullptr) {
+    CSA_REQUIRE(std::isfinite(theta) && theta > 1.0, "theta must be finite and > 1");
+    CSA_REQUIRE(scaling >= CSA_ROTARY_NONE && scaling <= CSA_ROTARY_RAMP, "scaling");
+    CSA_REQUIRE(scaling == CSA_ROTARY_NONE || (std::isfinite(factor) && factor >= 1.0),
+                "factor must be finite and >= 1");
+    if (scaling == CSA_ROTARY_TURNS || scaling == CSA_ROTARY_RAMP) {
+      CSA_REQUIRE(std::isfinite(orig_len) && orig_len >= 1.0, "orig_len must be finite and >= 1");
+      CSA_REQUIRE(low > 0.0 && high > low && std::isfinite(high), "0 < low < high");
+    }
+  }
+  CSA_TRY(check_ptr(freqs, "freqs", false));
+  CSA_TRY(check_ptr(table, "table"));
+  csa::Launch l;
+  CSA_TRY(launch_ctx(stream, &l));
+  return finish(csa::launch_rotary_table(l, rot, theta, scaling,
+                                         scaling == CSA_ROTARY_NONE ? 1.0 : factor, orig_len, low,
+                                         high, freqs, table),
+                "rotary table launch");
+}
+
+csa_status csa_rotary(const csa_rotary_desc* d, csa_stream stream) {
+  CSA_REQUIRE(d != nullptr, "the rotary descriptor is NULL");
+  CSA_REQUIRE(valid_dtype(d->dtype), "dtype");
+  CSA_REQUIRE(d->B >= 0 && d->S >= 0 && d->H >= 0 && d->H2 >= 0 && d->D > 0,
+              "B, S, H, H2 must be non-negative, D positive");
+  CSA_REQUIRE(d->D % 2 == 0, "D must be even");
+  CSA_SUPPORT(d->D <= 512, "D must be <= 512");
+  CSA_REQUIRE(d->rot >= 2 && d->rot % 2 == 0 && d->rot <= d->D, "rot must be even, 2 <= rot <= D");
+  CSA_REQUIRE(d->layout == CSA_ROTARY_HALF || d->layout == CSA_ROTARY_INTERLEAVED, "layout");
+  CSA_REQUIRE(std::isfinite(d->amplitude), "amplitude must be finite");
+  CSA_REQUIRE(d->positions == nullptr || d->pos_stride_b >= 0, "pos_stride_b must be non-negative");
+  if (d->B == 0 || d->S == 0 || (d->H == 0 && d->H2 == 0)) return CSA_OK;
+  CSA_SUPPORT(d->S <= (1ll << 30) && static_cast<int64_t>(d->B) * d->S <= (1ll << 29) / d->D,
+              "B * S * D must be <= 2^29");
+  CSA_SUPPORT(d->H <= 65535 && d->H2 <= 65535, "H and H2 must be <= 65535");
+  csa::RotaryArgs a;
+  if (d->H > 0) CSA_TRY(rotary_tensor(d, d->x, d->y, d->H, d->x_stride, d->y_stride, "x", &a.t[0]));
+  if (d->H2 > 0)
+    CSA_TRY(rotary_tensor(d, d->x2, d->y2, d->H2, d->x2_stride, d->y2_stride, "x2", &a.t[1]));
+  CSA_TRY(check_ptr(d->table, "table"));
+  CSA_TRY(check_ptr(d->positions, "positions", false, 4));
+  a.bf16 = d->dtype == CSA_BF16;
+  a.half = d->layout == CSA_ROTARY_HALF;
+  a.transpose = d->transpose != 0;
+  a.B = d->B;
+  a.S = d->S;
+  a.D = d->D;
+  a.rot = d->rot;
+  a.table = d->table;
+  a.amplitude = d->amplitude;
+  a.positions = d->positions;
+  a.pos_stride_b = d->pos_stride_b;
+  a.pos0 = d->pos0;
+  CSA_SUPPORT(csa::rotary_supported(a), "interleaved pairs must start on two elements' alignment");
+  csa::Launch l;
+  CSA_TRY(launch_ctx(stream, &l));
+  return finish(csa::launch_rotary(l, a), "rotary launch");
+}
+
+csa_status csa_cache_insert(const csa_cache_desc* c, const void* k, const int64_t* k_stride,
+                            const void* v, const int64_t* v_stride, csa_stream stream) {
+  CSA_TRY(cache_checks(c, true));
+  CSA_REQUIRE(k_stride != nullptr && v_stride != nullptr, "k_stride / v_stride is NULL");
+  if (c->B == 0) return CSA_OK;
+  Extent ek, ev, e1, e2;
+  CSA_TRY(cache_ptrs(c, true, &ek, &ev));
+  const int es = dtype_size(c->dtype);
+  CSA_TRY(check_ptr(k, "k", true, es));
+  CSA_TRY(check_ptr(v, "v", true, es));
+  const int64_t n[2] = {c->B, c->Hkv};
+  CSA_REQUIRE(extent_of(k, n, k_stride, 2, c->D, es, &e1) && extent_of(v, n, v_stride, 2, c->D, es, &e2),
+              "k / v: strides must be non-negative");
+  csa::Launch l;
+  CSA_TRY(launch_ctx(stream, &l));
+  return finish(csa::launch_cache_insert(l, cache_args(c), k, k_stride, v, v_stride),
+                "cache insert launch");
+}
+
+csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* s,
+                              csa_stream stream) {
+  CSA_TRY(cache_checks(c, false));
+  CSA_REQUIRE(s != nullptr, "the source descriptor is NULL");
+  CSA_REQUIRE(s->S >= 0, "S must be non-negative");
+  CSA_SUPPORT(s->S < 2147483648LL, "S must be < 2^31");
+  CSA_REQUIRE(s->positions == nullptr || s->next_pos != nullptr,
+              "source positions need the source's next_pos");
+  CSA_REQUIRE(s->len == nullptr || s->len != c->len, "the source's len must not be the cache's");
+  if (c->B == 0) return CSA_OK;
+  Extent ek, ev, sk, sv;
+  CSA_TRY(cache_ptrs(c, false, &ek, &ev));
+  if (s->S > 0) {
+    const int es = dtype_size(c->dtype);
+    CSA_TRY(check_ptr(s->K, "source K", true, es));
+    CSA_TRY(check_ptr(s->V, "source V", true, es));
+    CSA_TRY(check_ptr(s->weights, "source weights"));
+    const int64_t n[3] = {c->B, c->Hkv, s->S};
+    CSA_REQUIRE(extent_of(s->K, n, s->k_stride, 3, c->D, es, &sk) &&
+                    extent_of(s->V, n, s->v_stride, 3, c->D, es, &sv),
+                "source: strides must be non-negative");
+    const uintptr_t rows = static_cast<uintptr_t>(c->B) * c->Hkv;
+    auto dense = [&](const void* p, int64_t len) {
+      Extent x;
+      x.lo = reinterpret_cast<uintptr_t>(p);
+      x.hi = x.lo + rows * static_cast<uintptr_t>(len) * 4;
+      return x;
+    };
+    const Extent dw = dense(c->weights, c->T), dp = dense(c->positions, c->T);
+    const Extent sw = dense(s->weights, s->S);
+    CSA_REQUIRE(!sk.overlaps(ek) && !sk.overlaps(ev) && !sv.overlaps(ek) && !sv.overlaps(ev) &&
+                    !sw.overlaps(dw) && !sw.overlaps(dp),
+                "source and cache overlap");
+    if (s->positions) {
+      const Extent sp = dense(s->positions, s->S);
+      CSA_REQUIRE(!sp.overlaps(dp) && !sp.overlaps(dw), "source and cache overlap");
+    }
+  }
+  CSA_TRY(check_ptr(s->positions, "source positions", false));
+  CSA_TRY(check_ptr(s->len, "source len", false));
+  CSA_TRY(check_ptr(s->next_pos, "source next_pos", false));
+  csa::CacheSource a{};
+  a.K = s->K;
+  a.V = s->V;
+  for (int i = 0; i < 3; ++i) {
+    a.kst[i] = s->k_stride[i];
+    a.vst[i] = s->v_stride[i];
+  }
+  a.weights = s->weights;
+  a.positions = s->positions;
+  a.len = s->len;
+  a.next_pos = s->next_pos;
+  a.S = s->S;
+  csa::Launch l;
+  CSA_TRY(launch_ctx(stream, &l));
+  return finish(csa::launch_cache_compress(l, cache_args(c), a), "cache compress launch");
+}
+
+int64_t csa_prefix_decode_workspace_bytes(csa_dtype dtype, int B, int Hq, int Hkv, int D, int N,
+                                          int64_t Tp, int64_t T, int weights) {
+  if (prefix_sizes(dtype, B, Hq, Hkv, D, N, Tp, T) != CSA_OK) return -1;
+  csa::Launch l;
+  if (launch_ctx(nullptr, &l) != CSA_OK) return -1;
+  return csa::prefix_decode_workspace_bytes(dtype == CSA_BF16, B, Hkv, Hq / Hkv, D, N, T,
+                                            weights != 0, l.num_sms);
+}
+
+csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream) {
+  CSA_REQUIRE(d != nullptr, "the prefix decode descriptor is NULL");
+  CSA_TRY(prefix_sizes(d->dtype, d->B, d->Hq, d->Hkv, d->D, d->N, d->Tp, d->T));
+  CSA_REQUIRE(valid_dtype(d->out_dtype), "out_dtype");
+  CSA_REQUIRE(std::isfinite(d->scale) && d->scale > 0.f, "scale must be finite and positive");
+  CSA_REQUIRE(std::isfinite(d->decay) && d->decay >= 0.f, "decay must be finite and non-negative");
+  CSA_REQUIRE(d->N <= 1 || d->group_start != nullptr, "group_start is required for N > 1");
+  if (d->B == 0) return CSA_OK;
+  const int es = dtype_size(d->dtype);
+  if (d->N > 0 && d->Tp > 0) {
+    CSA_TRY(strides16(d->kp_stride, es, "Kp"));
+    CSA_TRY(strides16(d->vp_stride, es, "Vp"));
+    CSA_TRY(check_ptr(d->Kp, "Kp"));
+    CSA_TRY(check_ptr(d->Vp, "Vp"));
+  }
+  if (d->T > 0) {
+    CSA_TRY(strides16(d->k_stride, es, "K"));
+    CSA_TRY(strides16(d->v_stride, es, "V"));
+    CSA_TRY(check_ptr(d->K, "K"));
+    CSA_TRY(check_ptr(d->V, "V"));
+  }
+  CSA_TRY(check_ptr(d->q, "q"));
+  CSA_TRY(check_ptr(d->out, "out"));
+  CSA_TRY(check_ptr(d->prefix_len, "prefix_len", false));
+  CSA_TRY(check_ptr(d->group_start, "group_start", false));
+  CSA_TRY(check_ptr(d->len, "len", false));
+  CSA_TRY(check_ptr(d->lse_out, "lse_out", false));
+  CSA_TRY(check_ptr(d->weights, "weights", false));
+  CSA_TRY(check_ptr(d->workspace, "workspace"));
+  csa::Launch l;
+  CSA_TRY(launch_ctx(stream, &l));
+  const int G = d->Hq / d->Hkv;
+  CSA_REQUIRE(d->workspace_bytes >= csa::prefix_decode_workspace_bytes(
+                                        d->dtype == CSA_BF16, d->B, d->Hkv, G, d->D, d->N, d->T,
+                                        d->weights != nullptr, l.num_sms),
+              "workspace smaller than csa_prefix_decode_workspace_bytes()");
+  csa::PrefixDecodeArgs a{};
+  a.bf16 = d->dtype == CSA_BF16;
+  a.out_bf16 = d->out_dtype == CSA_BF16;
+  a.B = d->B;
+  a.Hq = d->Hq;
+  a.Hkv = d->Hkv;
+  a.D = d->D;
+  a.N = d->N;
+  a.scale = d->scale;
+  a.q = d->q;
+  a.Kp = d->Kp;
+  a.Vp = d->Vp;
+  a.K = d->K;
+  a.V = d->V;
+  for (int i = 0; i < 3; ++i) {
+    a.kps[i] = d->kp_stride[i];
+    a.vps[i] = d->vp_stride[i];
+    a.ks[i] = d->k_stride[i];
+    a.vs[i] = d->v_stride[i];
+  }
+  a.Tp = d->Tp;
+  a.T = d->T;
+  a.prefix_len = d->prefix_len;
+  a.group_start = d->group_start;
+  a.len = d->len;
+  a.out = d->out;
+  a.lse_out = d->lse_out;
+  a.weights = d->weights;
+  a.decay = d->decay;
+  a.workspace = d->workspace;
+  std::string why;
+  const cudaError_t e = csa::launch_prefix_decode(l, a, &why);
+  if (e != cudaSuccess && !why.empty()) return fail(CSA_ERR_CUDA, why);
+  return finish(e, "prefix decode launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,487 @@
+// A bounded KV cache kept by accumulated attention weight: one token in at a
+// time over the lightest (insert), or many rows into a smaller cache, the
+// heaviest kept (compress).
+//
+// A slot of unit u = (b, h) is protected when its token's position is below
+// n_sink or among the last n_local (>= next - n_local).  The others rank by
+// weight; NaN counts as -inf, equal weights go by the lower slot.  The rank
+// is taken on order-preserving 32-bit keys, so it is exact.
+#include <algorithm>
+
+#include "internal.h"
+
+namespace csa {
+namespace {
+
+constexpr uint32_t kKeyProtected = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  return w != w ? 0x007fffffu /* -inf's key */ : float_key(w);
+}
+
+__device__ __forceinline__ bool is_protected(int pos, int next, int n_sink, int n_local) {
+  return pos < n_sink || pos >= next - n_local;
+}
+
+// One row of `bytes` from src to dst by `n` threads (this one is `t`):
+// 16-byte words when every row starts on one, else two bytes at a time (the
+// narrowest element).
+__device__ __forceinline__ void copy_row(void* dst, const void* src, int bytes, bool wide, int t,
+                                         int n) {
+  if (wide) {
+    for (int i = t; i < bytes / 16; i += n)
+      static_cast<uint4*>(dst)[i] = static_cast<const uint4*>(src)[i];
+  } else {
+    for (int i = t; i < bytes / 2; i += n)
+      static_cast<uint16_t*>(dst)[i] = static_cast<const uint16_t*>(src)[i];
+  }
+}
+
+// ---------------------------------------------------------------- insert
+//
+// Reads the unit's weights and positions once (8 bytes a slot), so it is
+// bound by latency at the usual sizes: one CTA per unit, the minimum of
+// (key << 32 | slot) over its threads, four slots in flight per thread, then
+// the first warps write the new row.  The sequence's length and next position are shared
+// by its heads: each CTA reads them before it arrives at the sequence's
+// counter, and the last one to arrive advances them and clears the counter.
+constexpr int kInsThreads = 512;
+
+__global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
+    const CacheArgs c, const char* __restrict__ k, const char* __restrict__ v, int64_t kb,
+    int64_t kh, int64_t vb, int64_t vh, int wide, DevErr err) {
+  __shared__ int sh_len, sh_next;
+  __shared__ unsigned long long sh_best[kInsThreads / 32];
+  const int u = blockIdx.x, b = u / c.Hkv, h = u - b * c.Hkv, tid = threadIdx.x;
+  if (tid == 0) {
+    sh_len = *static_cast<volatile int32_t*>(c.len + b);
+    sh_next = *static_cast<volatile int32_t*>(c.next_pos + b);
+  }
+  __syncthreads();
+  const int len = sh_len, next = sh_next;
+  if (next < 0) return;  // an inactive sequence: nothing is read or written
+  if (len < 0 || len > c.budget) {
+    if (tid == 0) dev_flag(err, DEV_BAD_INDEX);
+    return;
+  }
+  int slot = len;
+  if (len == c.budget) {
+    const float* w = c.weights + static_cast<int64_t>(u) * c.T;
+    const int32_t* pos = c.positions + static_cast<int64_t>(u) * c.T;
+    unsigned long long best = ~0ull;
+    for (int j0 = tid; j0 < len; j0 += 4 * kInsThreads) {
+      float x[4];
+      int p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i * kInsThreads;
+        x[i] = j < len ? w[j] : 0.f;
+        p[i] = j < len ? pos[j] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i * kInsThreads;
+        if (j < len && !is_protected(p[i], next, c.n_sink, c.n_local)) {
+          const unsigned long long e =
+              (static_cast<unsigned long long>(weight_key(x[i])) << 32) | static_cast<unsigned>(j);
+          best = e < best ? e : best;
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long e = __shfl_xor_sync(0xffffffffu, best, o);
+      best = e < best ? e : best;
+    }
+    if ((tid & 31) == 0) sh_best[tid >> 5] = best;
+    __syncthreads();
+    best = sh_best[tid & (kInsThreads / 32 - 1)];
+#pragma unroll
+    for (int o = kInsThreads / 64; o > 0; o >>= 1) {
+      const unsigned long long e = __shfl_xor_sync(0xffffffffu, best, o);
+      best = e < best ? e : best;
+    }
+    slot = best == ~0ull ? -1 : static_cast<int>(best & 0xffffffffu);
+  }
+  if (slot >= 0) {
+    const int es = c.bf16 ? 2 : 4;
+    char* K = static_cast<char*>(c.K) + (b * c.kst[0] + h * c.kst[1] + slot * c.kst[2]) * es;
+    char* V = static_cast<char*>(c.V) + (b * c.vst[0] + h * c.vst[1] + slot * c.vst[2]) * es;
+    if (tid < 64)
+      copy_row(K, k + (b * kb + h * kh) * es, c.D * es, wide, tid, 64);
+    else if (tid < 128)
+      copy_row(V, v + (b * vb + h * vh) * es, c.D * es, wide, tid - 64, 64);
+    else if (tid == 128)
+      c.weights[static_cast<int64_t>(u) * c.T + slot] = 0.f;
+    else if (tid == 160)
+      c.positions[static_cast<int64_t>(u) * c.T + slot] = next;
+  } else if (tid == 0) {
+    dev_flag(err, DEV_BAD_INDEX);  // every slot protected: positions are not distinct
+  }
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(c.counters + b, 1) == c.Hkv - 1) {
+      __threadfence();
+      c.counters[b] = 0;
+      c.len[b] = len < c.budget ? len + 1 : len;
+      c.next_pos[b] = next + 1;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- compress
+//
+// Selection: one cluster of CS CTAs per unit, CTA r holding the keys of rows
+// [n r / CS, n (r + 1) / CS) in shared memory (re-read from memory when they
+// do not fit).  An MSB-first radix select over the keys' bytes finds the
+// budget-th largest key tau, the CTAs' histograms of each pass added through
+// distributed shared memory; keys equal to tau are taken lowest row first.
+// Each CTA writes its kept rows, ascending, into the destination's positions
+// (as row numbers; the copy turns them into positions).  The weights are
+// read once; bound by the passes' latency (4 cluster round trips).
+constexpr int kCmpThreads = 512;
+constexpr int kCmpKeys = 49152;  // keys held per CTA (192 KB)
+
+struct CompressParams {
+  const float* weights;        // [U, S]
+  const int32_t* positions;    // [U, S] or null: the row number
+  const int32_t* len;          // [B] or null: S
+  const int32_t* next_pos;     // [B] or null: the length
+  int64_t S;
+  int Hkv, budget, n_sink, n_local;
+  int64_t T;
+  int32_t* rows;               // destination positions [U, T]
+  int held;                    // keys are held in shared memory
+  DevErr err;
+};
+
+__device__ __forceinline__ int source_len(const int32_t* len, int b, int64_t S, const DevErr& e) {
+  if (len == nullptr) return static_cast<int>(S);
+  int n = len[b];
+  if (n < 0 || n > S) {
+    dev_flag(e, DEV_BAD_INDEX);
+    n = n < 0 ? 0 : static_cast<int>(S);
+  }
+  return n;
+}
+
+template <int CS>
+__global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const CompressParams p) {
+  if (CS > 1) cluster_arrive_relaxed();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ unsigned int hc[256], gc[256];
+  __shared__ unsigned int part_eq[CS], part_sel[CS];
+  __shared__ int scan_sh[33];
+  __shared__ unsigned int pick_sh[2];
+  const int rank = CS > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int u = blockIdx.x / CS, b = u / p.Hkv, tid = threadIdx.x, lane = tid & 31;
+  const int len = source_len(p.len, b, p.S, p.err);
+  const int next = p.next_pos ? p.next_pos[b] : len;
+  const int lo = static_cast<int>(static_cast<int64_t>(len) * rank / CS);
+  const int n = static_cast<int>(static_cast<int64_t>(len) * (rank + 1) / CS) - lo;
+  const float* wrow = p.weights + static_cast<int64_t>(u) * p.S + lo;
+  const int32_t* prow = p.positions ? p.positions + static_cast<int64_t>(u) * p.S + lo : nullptr;
+  auto make_key = [&](int j) -> uint32_t {
+    const int pos = prow ? prow[j] : lo + j;
+    return is_protected(pos, next, p.n_sink, p.n_local) ? kKeyProtected : weight_key(wrow[j]);
+  };
+  const bool select = len > p.budget;
+  int32_t* out = p.rows + static_cast<int64_t>(u) * p.T;
+  if (CS > 1) cluster_wait();  // every CTA of the cluster is running
+  if (!select) {  // uniform over the cluster: all rows stay
+    for (int j = tid; j < n; j += kCmpThreads) out[lo + j] = lo + j;
+    return;
+  }
+  const bool held = p.held != 0;
+  if (held)
+    for (int j = tid; j < n; j += kCmpThreads) keys[j] = make_key(j);
+  auto key_at = [&](int j) -> uint32_t { return held ? keys[j] : make_key(j); };
+  // keys > tau are taken, and the first `need` keys equal to tau
+  uint32_t prefix = 0u, mask = 0u;
+  unsigned int need = static_cast<unsigned int>(p.budget);
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int d = tid; d < 256; d += kCmpThreads) hc[d] = 0u;
+    __syncthreads();
+    for (int j0 = 0; j0 < n; j0 += kCmpThreads) {
+      const int j = j0 + tid;
+      int d = -1;
+      if (j < n) {
+        const uint32_t key = key_at(j);
+        if ((key & mask) == prefix) d = static_cast<int>((key >> shift) & 255u);
+      }
+      const unsigned int act = __ballot_sync(0xffffffffu, d >= 0);
+      if (d >= 0) {  // one shared atomic per distinct bucket of the warp
+        const unsigned int peers = __match_any_sync(act, d);
+        if (lane == __ffs(peers) - 1) atomicAdd(&hc[d], static_cast<unsigned int>(__popc(peers)));
+      }
+    }
+    if (CS > 1) {
+      cluster_arrive();  // every CTA's histogram of this pass is complete
+      cluster_wait();
+      for (int d = tid; d < 256; d += kCmpThreads) {
+        unsigned int cr[CS], cnt = 0u;
+#pragma unroll
+        for (int r = 0; r < CS; ++r) cr[r] = ld_cluster_u32(cluster_map(smem_u32(hc + d), r));
+#pragma unroll
+        for (int r = 0; r < CS; ++r) cnt += cr[r];
+        gc[d] = cnt;
+      }
+      cluster_arrive();  // every CTA has read the others' histograms (they may be cleared)
+      cluster_wait();
+    } else {
+      __syncthreads();
+      for (int d = tid; d < 256; d += kCmpThreads) gc[d] = hc[d];
+      __syncthreads();
+    }
+    if (tid < 32) {  // the bucket where the count from the top reaches `need`
+      unsigned int pc[8], lc = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        pc[i] = gc[255 - 8 * lane - i];
+        lc += pc[i];
+      }
+      unsigned int sc = lc;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned int t = __shfl_up_sync(0xffffffffu, sc, o);
+        if (lane >= o) sc += t;
+      }
+      unsigned int above = sc - lc;  // count in the buckets above this lane's eight
+      int sel = -1;
+      unsigned int above_sel = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (sel < 0) {
+          if (above + pc[i] >= need) {
+            sel = 255 - 8 * lane - i;
+            above_sel = above;
+          } else {
+            above += pc[i];
+          }
+        }
+      }
+      // `need` never exceeds the count of keys under the prefix: a bucket is hit
+      const unsigned int hit = __ballot_sync(0xffffffffu, sel >= 0);
+      if (lane == (hit ? __ffs(hit) - 1 : 0)) {
+        pick_sh[0] = sel < 0 ? 0u : static_cast<unsigned int>(sel);
+        pick_sh[1] = above_sel;
+      }
+    }
+    __syncthreads();
+    prefix |= pick_sh[0] << shift;
+    mask |= 255u << shift;
+    need -= pick_sh[1];
+    __syncthreads();  // pick_sh read before the next pass writes it
+  }
+  const uint32_t tau = prefix;
+  const int seg = (n + kCmpThreads - 1) / kCmpThreads;
+  const int s0 = min(n, tid * seg), s1 = min(n, s0 + seg);
+  int c_gt = 0, c_eq = 0;
+  for (int j = s0; j < s1; ++j) {
+    const uint32_t key = key_at(j);
+    c_gt += key > tau;
+    c_eq += key == tau;
+  }
+  int eq_tot = 0, eq_before = 0;
+  const int eq_base = block_exclusive_scan(c_eq, scan_sh, &eq_tot);
+  if (CS > 1) {
+    if (tid < CS)
+      st_cluster_u32(cluster_map(smem_u32(part_eq + rank), tid), static_cast<unsigned int>(eq_tot));
+    cluster_arrive();
+    cluster_wait();
+    for (int r = 0; r < rank; ++r) eq_before += static_cast<int>(part_eq[r]);
+  }
+  const int take = max(0, min(static_cast<int>(need) - eq_before, eq_tot));  // ties kept here
+  const int c_sel = c_gt + max(0, min(take - eq_base, c_eq));
+  int sel_tot = 0, sel_before = 0;
+  const int sel_base = block_exclusive_scan(c_sel, scan_sh, &sel_tot);
+  if (CS > 1) {
+    if (tid < CS)
+      st_cluster_u32(cluster_map(smem_u32(part_sel + rank), tid),
+                     static_cast<unsigned int>(sel_tot));
+    cluster_arrive();
+    cluster_wait();  // the last access to another CTA's shared memory is before this barrier
+    for (int r = 0; r < rank; ++r) sel_before += static_cast<int>(part_sel[r]);
+  }
+  int at = sel_before + sel_base, eq_seen = eq_base;
+  for (int j = s0; j < s1; ++j) {
+    const uint32_t key = key_at(j);
+    bool t = key > tau;
+    if (key == tau) {
+      t = eq_seen < take;
+      ++eq_seen;
+    }
+    if (t) {
+      if (at < p.budget) out[at] = lo + j;
+      ++at;
+    }
+  }
+}
+
+// Copy: destination slot i of unit u gets source row rows[u, i] (K, V, the
+// weight), and rows[u, i] becomes the row's position.  Bound by HBM: a warp
+// takes kCopyRows rows, half of its lanes the K rows and half the V rows,
+// every load of the warp in flight before its first store.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyRows = 4;
+
+struct CopyParams {
+  CacheArgs dst;
+  const char *K, *V;
+  int64_t kst[3], vst[3];
+  const float* weights;
+  const int32_t* positions;
+  const int32_t* len;
+  const int32_t* next_pos;
+  int64_t S;
+  int wide;
+  DevErr err;
+};
+
+__global__ void __launch_bounds__(kCopyThreads) compress_copy_kernel(const CopyParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the row numbers are written
+  const CacheArgs& d = p.dst;
+  const int u = blockIdx.y, b = u / d.Hkv, h = u - b * d.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = source_len(p.len, b, p.S, p.err);
+  const int kept = min(len, d.budget);
+  const int i0 = (blockIdx.x * (kCopyThreads / 32) + warp) * kCopyRows;
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
+    const int next = p.next_pos ? p.next_pos[b] : len;
+    d.len[b] = kept;
+    if (d.next_pos) d.next_pos[b] = next;
+  }
+  if (i0 >= kept) return;
+  int32_t* rows = d.positions + static_cast<int64_t>(u) * d.T;
+  const int es = d.bf16 ? 2 : 4, bytes = d.D * es;
+  const int nr = min(kCopyRows, kept - i0);
+  int mine = lane < nr ? rows[i0 + lane] : 0;
+  if (lane < nr) {
+    if (mine < 0 || mine >= len) {  // cannot happen; never read past the source
+      dev_flag(p.err, DEV_BAD_INDEX);
+      mine = 0;
+    }
+    const int64_t src = static_cast<int64_t>(u) * p.S + mine;
+    d.weights[static_cast<int64_t>(u) * d.T + i0 + lane] = p.weights[src];
+    rows[i0 + lane] = p.positions ? p.positions[src] : mine;
+  }
+  const bool is_v = lane >= 16;
+  const int t = lane & 15;
+  const char* sp = is_v ? p.V + (b * p.vst[0] + h * p.vst[1]) * es
+                        : p.K + (b * p.kst[0] + h * p.kst[1]) * es;
+  char* dp = is_v ? static_cast<char*>(d.V) + (b * d.vst[0] + h * d.vst[1]) * es
+                  : static_cast<char*>(d.K) + (b * d.kst[0] + h * d.kst[1]) * es;
+  const int64_t ss = (is_v ? p.vst[2] : p.kst[2]) * es, ds = (is_v ? d.vst[2] : d.kst[2]) * es;
+  int row[kCopyRows];
+#pragma unroll
+  for (int r = 0; r < kCopyRows; ++r) row[r] = __shfl_sync(0xffffffffu, mine, r);
+  if (p.wide) {
+    for (int o = t * 16; o < bytes; o += 256) {
+      uint4 x[kCopyRows];
+#pragma unroll
+      for (int r = 0; r < kCopyRows; ++r)
+        if (r < nr) x[r] = __ldcs(reinterpret_cast<const uint4*>(sp + row[r] * ss + o));
+#pragma unroll
+      for (int r = 0; r < kCopyRows; ++r)
+        if (r < nr) *reinterpret_cast<uint4*>(dp + (i0 + r) * ds + o) = x[r];
+    }
+  } else {
+    for (int r = 0; r < nr; ++r) copy_row(dp + (i0 + r) * ds, sp + row[r] * ss, bytes, false, t, 16);
+  }
+}
+
+template <int CS>
+cudaError_t launch_compress_select(const Launch& l, const CompressParams& p, int U, size_t smem) {
+  const void* fn = reinterpret_cast<const void*>(compress_select_kernel<CS>);
+  if (smem > 40 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(U) * CS);
+  cfg.blockDim = dim3(kCmpThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = l.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, compress_select_kernel<CS>, p);
+}
+
+// Rows of `st`-strided tensors at `ptr` all start on a 16-byte boundary.
+bool rows_wide(const void* ptr, const int64_t* st, int n, int es, int D) {
+  bool ok = reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && (D * es) % 16 == 0;
+  for (int i = 0; i < n; ++i) ok = ok && (st[i] * es) % 16 == 0;
+  return ok;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_insert(const Launch& l, const CacheArgs& c, const void* k,
+                                const int64_t* kst, const void* v, const int64_t* vst) {
+  const int es = c.bf16 ? 2 : 4;
+  const bool wide = rows_wide(c.K, c.kst, 3, es, c.D) && rows_wide(c.V, c.vst, 3, es, c.D) &&
+                    rows_wide(k, kst, 2, es, c.D) && rows_wide(v, vst, 2, es, c.D);
+  cache_insert_kernel<<<c.B * c.Hkv, kInsThreads, 0, l.stream>>>(
+      c, static_cast<const char*>(k), static_cast<const char*>(v), kst[0], kst[1], vst[0], vst[1],
+      wide ? 1 : 0, l.err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_compress(const Launch& l, const CacheArgs& dst, const CacheSource& s) {
+  const int U = dst.B * dst.Hkv, es = dst.bf16 ? 2 : 4;
+  if (s.S > 0) {
+    CompressParams p{s.weights, s.positions,  s.len,       s.next_pos, s.S,           dst.Hkv,
+                     dst.budget, dst.n_sink, dst.n_local, dst.T,      dst.positions, 0,
+                     l.err};
+    // CTAs per unit: about 4096 rows each, while the units alone leave SMs idle
+    int CS = 1;
+    while (CS < 8 && s.S > 4096ll * CS && 2ll * U * CS <= 2ll * l.num_sms) CS *= 2;
+    while (CS < 8 && (s.S + CS - 1) / CS > kCmpKeys) CS *= 2;
+    const int64_t per = (s.S + CS - 1) / CS;
+    p.held = per <= kCmpKeys ? 1 : 0;
+    const size_t smem = p.held ? static_cast<size_t>(per) * 4 : 0;
+    const cudaError_t e = CS == 1   ? launch_compress_select<1>(l, p, U, smem)
+                          : CS == 2 ? launch_compress_select<2>(l, p, U, smem)
+                          : CS == 4 ? launch_compress_select<4>(l, p, U, smem)
+                                    : launch_compress_select<8>(l, p, U, smem);
+    if (e != cudaSuccess) return e;
+  }
+  CopyParams p{};
+  p.dst = dst;
+  p.K = static_cast<const char*>(s.K);
+  p.V = static_cast<const char*>(s.V);
+  for (int i = 0; i < 3; ++i) {
+    p.kst[i] = s.kst[i];
+    p.vst[i] = s.vst[i];
+  }
+  p.weights = s.weights;
+  p.positions = s.positions;
+  p.len = s.len;
+  p.next_pos = s.next_pos;
+  p.S = s.S;
+  p.wide = rows_wide(dst.K, dst.kst, 3, es, dst.D) && rows_wide(dst.V, dst.vst, 3, es, dst.D) &&
+           rows_wide(s.K, s.kst, 3, es, dst.D) && rows_wide(s.V, s.vst, 3, es, dst.D);
+  p.err = l.err;
+  const int64_t most = std::min<int64_t>(dst.budget, s.S);
+  const int per_block = kCopyThreads / 32 * kCopyRows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, (most + per_block - 1) / per_block)),
+                     static_cast<unsigned>(U));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = l.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, compress_copy_kernel, p);
+}
+
+}  // namespace csa

@@ -96,6 +96,75 @@ cudaError_t launch_tsa_scatter(const Launch& l, const void* Oc, const int32_t* i
 cudaError_t launch_rope(const Launch& l, const void* x, void* y, bool bf16, int64_t rows, int D,
                         int64_t period, int64_t pos0, float theta);
 
+// rotary.cu
+enum RotScaling : int { ROT_NONE = 0, ROT_LINEAR = 1, ROT_NTK = 2, ROT_TURNS = 3, ROT_RAMP = 4 };
+struct RotaryArgs {
+  struct Tensor {  // H = 0: none
+    const void* x = nullptr;
+    void* y = nullptr;
+    int H = 0;
+    int64_t xst[3] = {0, 0, 0};  // batch, token, head strides in elements
+    int64_t yst[3] = {0, 0, 0};
+  } t[2];
+  bool bf16 = true, half = true, transpose = false;
+  int64_t B = 0, S = 0;
+  int D = 0, rot = 0;
+  const uint64_t* table = nullptr;
+  float amplitude = 1.f;
+  const int32_t* positions = nullptr;
+  int64_t pos_stride_b = 0, pos0 = 0;
+};
+// rot/2 entries: the fraction of a turn per position, in units of 2^-64;
+// from `freqs` (radians per position) when given, else from the formula.
+cudaError_t launch_rotary_table(const Launch& l, int rot, double theta, int scaling, double factor,
+                                double orig_len, double low, double high, const double* freqs,
+                                uint64_t* table);
+// Interleaved pairs need every pair aligned to its two elements.
+bool rotary_supported(const RotaryArgs& a);
+cudaError_t launch_rotary(const Launch& l, const RotaryArgs& a);
+
+// cache.cu
+// A bounded cache: K, V [B, Hkv, T, D] by strides (elements: b, h, slot),
+// weights and positions [B, Hkv, T] dense, len / next_pos / counters [B].
+struct CacheArgs {
+  void *K, *V;
+  int64_t kst[3], vst[3];
+  float* weights;
+  int32_t *positions, *len, *next_pos, *counters;
+  bool bf16;
+  int B, Hkv, D, budget, n_sink, n_local;
+  int64_t T;
+};
+struct CacheSource {  // rows to compress; weights and positions [B, Hkv, S] dense
+  const void *K, *V;
+  int64_t kst[3], vst[3];
+  const float* weights;
+  const int32_t *positions, *len, *next_pos;  // each may be null
+  int64_t S;
+};
+cudaError_t launch_cache_insert(const Launch& l, const CacheArgs& c, const void* k,
+                                const int64_t* kst, const void* v, const int64_t* vst);
+cudaError_t launch_cache_compress(const Launch& l, const CacheArgs& dst, const CacheSource& s);
+
+// prefix_decode.cu
+struct PrefixDecodeArgs {
+  bool bf16, out_bf16;
+  int B, Hq, Hkv, D, N;
+  float scale;
+  const void* q;                            // [B, Hq, D]
+  const void *Kp, *Vp, *K, *V;
+  int64_t kps[3], vps[3], ks[3], vs[3];     // strides: prefix / sequence, head, token
+  int64_t Tp, T;
+  const int32_t *prefix_len, *group_start, *len;
+  void* out;
+  float *lse_out, *weights;
+  float decay;
+  void* workspace;
+};
+int64_t prefix_decode_workspace_bytes(bool bf16, int B, int Hkv, int G, int D, int N, int64_t T,
+                                      bool weights, int num_sms);
+cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std::string* why);
+
 // decode.cu
 int decode_default_parts(bool bf16, int D, int L, int num_sms);
 // Merged mode: the last CTA of each unit combines the unit's splits.

@@ -1,0 +1,271 @@
+// Rotary positions for queries and keys: both pair layouts, part of the head,
+// scaled frequencies, strided views, and the transposed rotation (the
+// gradient).
+//
+// Pair i (i < rot/2) of a token at position p turns by t = p w_i:
+//   y_a = A (x_a cos t - x_b sin t),  y_b = A (x_b cos t + x_a sin t),
+// (a, b) = (i, i + rot/2) or (2i, 2i + 1); values past rot are copied.
+//
+// Angles.  cos and sin only need p w_i modulo one turn, so a frequency is
+// held as the 64-bit fraction of a turn per position (w / 2 pi * 2^64) and
+// p w_i is one integer product that wraps by itself: exact modulo a turn
+// for any 32-bit position (also a negative one), 2^-33 turns of error at
+// p = 2^31 from the table's rounding.  The top 32 bits, as a float in
+// [-1, 1) half turns, go to sincospif: no range reduction, no 64-bit float.
+//
+// Bound by HBM: 2 * bytes(q, k).  A thread keeps the sines and cosines of
+// its V pairs in registers and runs over the heads (stride J), so a token's
+// angles are formed once per J heads' worth of threads; loads are up to 16
+// bytes, four heads in flight.
+#include <algorithm>
+
+#include "internal.h"
+
+namespace csa {
+namespace {
+
+constexpr int kRotThreads = 256;
+
+struct RotTensor {
+  const void* x;
+  void* y;
+  int H;
+  int64_t xb, xs, xh, yb, ys, yh;  // strides in elements
+};
+
+struct RotParams {
+  RotTensor t[2];
+  uint32_t tokens, S;
+  uint32_t J, nrot, ntail;  // threads per token along the heads; V-wide chunks: rotated, copied
+  int rot;
+  const uint64_t* table;
+  float amp, sgn;
+  const int32_t* positions;
+  int64_t pos_b;
+  int64_t pos0;
+};
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v) { return static_cast<float>(v); }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// HALF: V pairs from two V-wide accesses rot/2 apart; otherwise V/2 pairs
+// from one V-wide access.
+template <typename T, int V, bool HALF>
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotParams p) {
+  constexpr int NP = HALF ? V : V / 2;
+  const uint32_t nchunk = p.nrot + p.ntail;
+  const uint32_t id = blockIdx.x * kRotThreads + threadIdx.x;  // B S D <= 2^29: fits 32 bits
+  const uint32_t slot = id / nchunk, c = id - slot * nchunk;
+  const uint32_t tok = slot / p.J;
+  const int j = static_cast<int>(slot - tok * p.J);
+  if (tok >= p.tokens) return;
+  const int64_t b = tok / p.S, s = tok % p.S;
+  const int H = p.t[0].H + p.t[1].H, J = static_cast<int>(p.J);
+  using VT = Vec<T, V>;
+  const bool tail = c >= p.nrot;
+  float cs[NP], sn[NP];
+  if (!tail) {
+    const int64_t pos = p.positions ? static_cast<int64_t>(p.positions[b * p.pos_b + s]) : p.pos0 + s;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(p.table + c * NP + i);
+      const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+      float sv, cv;
+      sincospif(half_turns, &sv, &cv);
+      cs[i] = cv * p.amp;
+      sn[i] = sv * p.amp * p.sgn;
+    }
+  }
+  const int e0 = static_cast<int>(tail ? p.rot + (c - p.nrot) * V : c * V);  // first element of the (first) access
+  constexpr int U = 4;
+  for (int h0 = j; h0 < H; h0 += U * J) {
+    VT u[U], w[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int h = h0 + k * J;
+      if (h < H) {
+        const RotTensor& t = h < p.t[0].H ? p.t[0] : p.t[1];
+        const int hh = h < p.t[0].H ? h : h - p.t[0].H;
+        const T* x = static_cast<const T*>(t.x) + b * t.xb + s * t.xs + hh * t.xh + e0;
+        u[k] = *reinterpret_cast<const VT*>(x);
+        if (HALF && !tail) w[k] = *reinterpret_cast<const VT*>(x + p.rot / 2);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int h = h0 + k * J;
+      if (h < H) {
+        const RotTensor& t = h < p.t[0].H ? p.t[0] : p.t[1];
+        const int hh = h < p.t[0].H ? h : h - p.t[0].H;
+        T* y = static_cast<T*>(t.y) + b * t.yb + s * t.ys + hh * t.yh + e0;
+        if (!tail) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const float a = to_f(HALF ? u[k].v[i] : u[k].v[2 * i]);
+            const float d = to_f(HALF ? w[k].v[i] : u[k].v[2 * i + 1]);
+            const T ya = from_f<T>(a * cs[i] - d * sn[i]);
+            const T yd = from_f<T>(d * cs[i] + a * sn[i]);
+            if (HALF) {
+              u[k].v[i] = ya;
+              w[k].v[i] = yd;
+            } else {
+              u[k].v[2 * i] = ya;
+              u[k].v[2 * i + 1] = yd;
+            }
+          }
+        }
+        *reinterpret_cast<VT*>(y) = u[k];
+        if (HALF && !tail) *reinterpret_cast<VT*>(y + p.rot / 2) = w[k];
+      }
+    }
+  }
+}
+
+struct TableParams {
+  int n, rot, scaling;
+  double theta, factor, orig_len, low, high;
+  const double* freqs;
+  uint64_t* table;
+};
+
+__global__ void rotary_table_kernel(const TableParams p) {
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= p.n) return;
+  double w;
+  if (p.freqs != nullptr) {
+    w = p.freqs[i];
+  } else {
+    const double e = -2.0 * i / p.rot;
+    w = pow(p.theta, e);
+    double keep = 1.0;  // share of the unscaled frequency
+    switch (p.scaling) {
+      case ROT_LINEAR:
+        keep = 0.0;
+        break;
+      case ROT_NTK:
+        w = p.rot > 2 ? pow(p.theta * pow(p.factor, p.rot / (p.rot - 2.0)), e) : 1.0;
+        break;
+      case ROT_TURNS:
+        keep = (p.orig_len * w / kTwoPi - p.low) / (p.high - p.low);
+        break;
+      case ROT_RAMP: {
+        const double lt = 2.0 * log(p.theta);
+        const double lo = fmax(0.0, floor(p.rot * log(p.orig_len / (p.high * kTwoPi)) / lt));
+        const double hi = fmin(p.rot - 1.0, ceil(p.rot * log(p.orig_len / (p.low * kTwoPi)) / lt));
+        keep = 1.0 - (i - lo) / fmax(hi - lo, 0.001);
+        break;
+      }
+      default:
+        break;
+    }
+    keep = fmin(1.0, fmax(0.0, keep));
+    w = w / p.factor * (1.0 - keep) + w * keep;
+  }
+  double t = w / kTwoPi;
+  t -= floor(t);  // whole turns fall away
+  const double f = rint(t * 0x1p64);
+  p.table[i] = f >= 0x1p64 ? 0ull : static_cast<uint64_t>(f);
+}
+
+template <typename T, int V>
+cudaError_t launch_v(const Launch& l, const RotParams& p, bool half) {
+  const int64_t threads = static_cast<int64_t>(p.tokens) * p.J * (p.nrot + p.ntail);
+  const int64_t grid = (threads + kRotThreads - 1) / kRotThreads;
+  if (half) {
+    rotary_kernel<T, V, true><<<static_cast<unsigned>(grid), kRotThreads, 0, l.stream>>>(p);
+  } else {
+    // a pair is two neighbours: the one-element width does not occur
+    if constexpr (V >= 2)
+      rotary_kernel<T, V, false><<<static_cast<unsigned>(grid), kRotThreads, 0, l.stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const Launch& l, const RotParams& p, bool half, int V) {
+  switch (V) {
+    case 8:
+      if constexpr (sizeof(T) == 2) return launch_v<T, 8>(l, p, half);
+      return cudaErrorInvalidValue;
+    case 4: return launch_v<T, 4>(l, p, half);
+    case 2: return launch_v<T, 2>(l, p, half);
+    default: return launch_v<T, 1>(l, p, half);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rotary_table(const Launch& l, int rot, double theta, int scaling, double factor,
+                                double orig_len, double low, double high, const double* freqs,
+                                uint64_t* table) {
+  const int n = rot / 2;
+  TableParams p{n, rot, scaling, theta, factor, orig_len, low, high, freqs, table};
+  rotary_table_kernel<<<(n + 127) / 128, 128, 0, l.stream>>>(p);
+  return cudaGetLastError();
+}
+
+// The widest access that every row, pair half and stride allows.
+static int rotary_width(const RotaryArgs& a) {
+  int V = a.bf16 ? 8 : 4;
+  auto ok = [&](int64_t n) { return n % V == 0; };
+  const int64_t edge = a.half ? a.rot / 2 : a.rot;
+  for (; V > 1; V /= 2) {
+    bool good = ok(edge) && ok(a.D - a.rot);
+    for (int k = 0; k < 2; ++k)
+      if (a.t[k].H > 0) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(a.t[k].x) | reinterpret_cast<uintptr_t>(a.t[k].y);
+        good = good && at % (static_cast<uintptr_t>(V) * (a.bf16 ? 2 : 4)) == 0;
+        for (int i = 0; i < 3; ++i) good = good && ok(a.t[k].xst[i]) && ok(a.t[k].yst[i]);
+      }
+    if (good) break;
+  }
+  return V;
+}
+
+bool rotary_supported(const RotaryArgs& a) { return a.half || rotary_width(a) >= 2; }
+
+cudaError_t launch_rotary(const Launch& l, const RotaryArgs& a) {
+  RotParams p{};
+  bool in_place = true;
+  int H = 0;
+  for (int k = 0; k < 2; ++k) {
+    const auto& t = a.t[k];
+    p.t[k] = RotTensor{t.x,      t.y,      t.H,      t.xst[0], t.xst[1], t.xst[2],
+                       t.yst[0], t.yst[1], t.yst[2]};
+    H += t.H;
+    if (t.H > 0 && t.x != t.y) in_place = false;
+  }
+  const int V = rotary_width(a);
+  p.tokens = static_cast<uint32_t>(a.B * a.S);
+  p.S = static_cast<uint32_t>(a.S);
+  p.rot = a.rot;
+  p.nrot = a.half ? a.rot / 2 / V : a.rot / V;
+  p.ntail = in_place ? 0 : (a.D - a.rot) / V;  // in place, the copied part is there already
+  p.table = a.table;
+  p.amp = a.amplitude;
+  p.sgn = a.transpose ? -1.f : 1.f;
+  p.positions = a.positions;
+  p.pos_b = a.pos_stride_b;
+  p.pos0 = a.pos0;
+  // Heads side by side: four keep a warp's accesses in long runs; more when
+  // the tokens alone are too few to fill the SMs.
+  const int64_t per_token = p.nrot + p.ntail;
+  const int64_t want = 1024ll * l.num_sms;
+  const int64_t lanes = p.tokens * per_token;
+  p.J = static_cast<uint32_t>(std::min<int64_t>(H, std::max<int64_t>(4, (want + lanes - 1) / lanes)));
+  return a.bf16 ? launch_t<__nv_bfloat16>(l, p, a.half, V) : launch_t<float>(l, p, a.half, V);
+}
+
+}  // namespace csa

@@ -4,8 +4,10 @@
 summaries, scores, index lists, split-K partials, outputs) and runs a step
 as: score -> select (top-k / top-p / hierarchical) -> sparse decode ->
 LSE merge.  ``BlockSparsePrefill`` runs tile means -> causal scores -> top-k
--> block-sparse prefill.  Buffers come from torch (device memory); every
-computation is a call into libcsa.
+-> block-sparse prefill.  ``Rotary``, ``TokenCache`` and ``SharedPrefixDecoder``
+serve sequences that share prefixes: positions, a cache of their own bounded
+by attention weight, and the decode over both.  Buffers come from torch (device
+memory); every computation is a call into libcsa.
 """
 from __future__ import annotations
 
@@ -287,3 +289,205 @@ class BlockSparsePrefill:
         self.select_chunks(stream)
         self.attend(stream)
         return self.O
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        csa._need(t is None or t.device == device, f"{name} is on {None if t is None else t.device}, not {device}")
+
+
+def _rows(name, t, dtype, shape=None):
+    """A tensor whose last index is dense: its other strides, in elements."""
+    csa._need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    csa._need(shape is None or tuple(t.shape) == tuple(shape),
+              f"{name} must have shape {shape}, not {None if shape is None else tuple(t.shape)}")
+    csa._need(t.stride(-1) == 1 or t.shape[-1] == 1, f"{name}: the last index must be dense")
+    return t.stride()[:-1]
+
+
+def _dense(name, t, dtype, shape):
+    csa._need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    csa._need(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    csa._need(t.is_contiguous(), f"{name} must be contiguous")
+    return t
+
+
+class Rotary:
+    """Rotary positions (csa_rotary) with one frequency table.
+
+    rot: values of each head that turn (the rest is copied); layout "half" or
+    "interleaved" pairs; scaling "none", "linear", "ntk", "turns" or "ramp"
+    with `factor` (and orig_len, low, high), or ``freqs`` (rot/2 fp64 radians per
+    position) for any other rule; amplitude multiplies the turned values."""
+
+    def __init__(self, rot: int, *, theta: float = 10000.0, layout: str = "half",
+                 scaling: str = "none", factor: float = 1.0, orig_len: float = 8192,
+                 low: float = 1.0, high: float = 32.0, amplitude: float = 1.0,
+                 freqs: torch.Tensor | None = None, device="cuda"):
+        self.rot, self.layout, self.amplitude = rot, csa._ROTARY_LAYOUT[layout], float(amplitude)
+        self.table = torch.empty(rot // 2, dtype=torch.int64, device=device)
+        if freqs is not None:
+            freqs = _dense("freqs", freqs, torch.float64, (rot // 2,))
+        with torch.cuda.device(self.table.device):
+            csa.csa_rotary_table(rot, theta, scaling, factor, orig_len, low, high, freqs,
+                                 self.table)
+
+    def rotate(self, q: torch.Tensor, k: torch.Tensor | None = None, *,
+               positions: torch.Tensor | None = None, pos0: int = 0, q_out=None, k_out=None,
+               transpose: bool = False, stream=None):
+        """Turns q [B, S, Hq, D] and k [B, S, Hkv, D] (any strides, the last
+        index dense; a decode step has S = 1) in one launch.  positions: int32
+        [B, S] (rows may repeat: expand a [1, S]), else pos0 + s.  Results go to
+        q_out / k_out (q_out=q: in place), new tensors by default.
+        transpose=True gives the gradient of the input from that of the output.
+        Returns (q_out, k_out), or q_out alone without k."""
+        B, S, Hq, D = q.shape
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        d = csa.RotaryDesc()
+        d.x, d.y, d.H = q.data_ptr(), q_out.data_ptr(), Hq
+        d.x_stride = csa._st3(*_rows("q", q, q.dtype))
+        d.y_stride = csa._st3(*_rows("q_out", q_out, q.dtype, q.shape))
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            d.x2, d.y2, d.H2 = k.data_ptr(), k_out.data_ptr(), k.shape[2]
+            d.x2_stride = csa._st3(*_rows("k", k, q.dtype, (B, S, k.shape[2], D)))
+            d.y2_stride = csa._st3(*_rows("k_out", k_out, q.dtype, k.shape))
+        _same_device(self.table.device, q=q, q_out=q_out, k=k, k_out=k_out, positions=positions)
+        if positions is not None:
+            csa._need(positions.dtype == torch.int32 and tuple(positions.shape) == (B, S),
+                      f"positions must be int32 of shape {(B, S)}")
+            csa._need(S == 1 or positions.stride(1) == 1, "positions: the token index must be dense")
+            d.positions, d.pos_stride_b = positions.data_ptr(), positions.stride(0)
+        d.dtype, d.B, d.S, d.D, d.rot = csa._dt(q.dtype), B, S, D, self.rot
+        d.layout, d.transpose, d.table = self.layout, int(transpose), self.table.data_ptr()
+        d.amplitude, d.pos0 = self.amplitude, pos0
+        csa.csa_rotary(d, stream=stream)
+        return q_out if k is None else (q_out, k_out)
+
+
+class TokenCache:
+    """A KV cache bounded by accumulated attention weight (csa_cache_insert,
+    csa_cache_compress).
+
+    K, V: [B, Hkv, T, D] bf16 or fp32, any strides with the last index dense
+    ([B, T, Hkv, D] storage as a transposed view).  lengths [B] int32 slots in
+    use, next_pos [B] int32 (the next token's position; negative: inactive),
+    positions [B, Hkv, T] int32 and weights [B, Hkv, T] fp32: made here (empty
+    cache, positions from 0) unless given; all are updated in place.  Slots are
+    in no order; ``positions`` says where each token stands.  budget: slots kept
+    (default T), the protected first n_sink positions and last n_local tokens
+    among them."""
+
+    def __init__(self, K: torch.Tensor, V: torch.Tensor, *, lengths=None, next_pos=None,
+                 positions=None, weights=None, budget: int | None = None, n_sink: int = 0,
+                 n_local: int = 0):
+        B, Hkv, T, D = K.shape
+        dev = K.device
+
+        def own(name, t, dtype, shape):
+            return torch.zeros(shape, dtype=dtype, device=dev) if t is None else _dense(name, t, dtype, shape)
+
+        self.K, self.V, self.B, self.Hkv, self.T, self.D = K, V, B, Hkv, T, D
+        self.lengths = own("lengths", lengths, torch.int32, (B,))
+        self.next_pos = own("next_pos", next_pos, torch.int32, (B,))
+        self.positions = own("positions", positions, torch.int32, (B, Hkv, T))
+        self.weights = own("weights", weights, torch.float32, (B, Hkv, T))
+        self.counters = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.budget = T if budget is None else budget
+        self.k_stride, self.v_stride = _rows("K", K, K.dtype), _rows("V", V, K.dtype, K.shape)
+        _same_device(dev, V=V, lengths=lengths, next_pos=next_pos, positions=positions, weights=weights)
+        self.desc = csa.cache_desc(
+            K=K, V=V, dtype=K.dtype, B=B, Hkv=Hkv, D=D, T=T, k_stride=self.k_stride,
+            v_stride=self.v_stride, weights=self.weights, positions=self.positions,
+            len=self.lengths, next_pos=self.next_pos, budget=self.budget, n_sink=n_sink,
+            n_local=n_local, counters=self.counters)
+
+    def insert(self, k: torch.Tensor, v: torch.Tensor, stream=None):
+        """One new token per active sequence, k and v [B, Hkv, D] (the last
+        index dense): into the next free slot, or over the lightest unprotected."""
+        shape = (self.B, self.Hkv, self.D)
+        ks, vs = _rows("k", k, self.K.dtype, shape), _rows("v", v, self.K.dtype, shape)
+        csa.csa_cache_insert(self.desc, k, ks, v, vs, stream=stream)
+
+    def compress(self, K: torch.Tensor, V: torch.Tensor, weights: torch.Tensor, *, lengths=None,
+                 positions=None, next_pos=None, stream=None):
+        """Fills this cache from longer K, V [B, Hkv, S, D] with weights [B, Hkv,
+        S] (a prompt's, as csa_token_importance gives them, or another cache's):
+        all rows below `lengths`, or the protected and the heaviest ones up to
+        the budget, in row order.  positions [B, Hkv, S] with next_pos [B], else
+        the row numbers."""
+        B, Hkv, S, D = K.shape
+        csa._need((B, Hkv, D) == (self.B, self.Hkv, self.D), "source K has other sizes than the cache")
+        src = csa.cache_source(
+            K=K, V=V, S=S, k_stride=_rows("source K", K, self.K.dtype),
+            v_stride=_rows("source V", V, self.K.dtype, K.shape),
+            weights=_dense("source weights", weights, torch.float32, (B, Hkv, S)),
+            positions=positions if positions is None else _dense("source positions", positions, torch.int32, (B, Hkv, S)),
+            len=lengths if lengths is None else _dense("source lengths", lengths, torch.int32, (B,)),
+            next_pos=next_pos if next_pos is None else _dense("source next_pos", next_pos, torch.int32, (B,)))
+        csa.csa_cache_compress(self.desc, src, stream=stream)
+
+
+class SharedPrefixDecoder:
+    """Decode steps of sequences that share prefixes, over a ``TokenCache``
+    (csa_prefix_decode).
+
+    Kp, Vp: [N, Hkv, Tp, D] in the cache's dtype (any strides, last index
+    dense), prefix_len [N] int32 (default Tp), group_start [N + 1] int32:
+    sequences group_start[n] .. group_start[n+1]-1 share prefix n (default: one
+    prefix for all).  accumulate: add each step's attention weights on the own
+    slots to cache.weights, the old sums times `decay` first.  rotary: turns
+    the queries and new keys of ``step`` at cache.next_pos."""
+
+    def __init__(self, cache: TokenCache, *, Hq: int, Kp=None, Vp=None, prefix_len=None,
+                 group_start=None, accumulate: bool = True, decay: float = 1.0,
+                 scale: float | None = None, out_dtype=torch.float32, rotary: Rotary | None = None):
+        B, Hkv, T, D, dt, dev = cache.B, cache.Hkv, cache.T, cache.D, cache.K.dtype, cache.K.device
+        self.cache, self.Hq, self.rotary = cache, Hq, rotary
+        N = Tp = 0
+        kw = {}
+        if Kp is not None:
+            N, _, Tp, _ = Kp.shape
+            csa._need(Vp is not None, "Kp without Vp")
+            kw = dict(Kp=Kp, Vp=Vp, kp_stride=_rows("Kp", Kp, dt, (N, Hkv, Tp, D)),
+                      vp_stride=_rows("Vp", Vp, dt, Kp.shape))
+            if prefix_len is not None:
+                kw["prefix_len"] = _dense("prefix_len", prefix_len, torch.int32, (N,))
+            if group_start is not None:
+                kw["group_start"] = _dense("group_start", group_start, torch.int32, (N + 1,))
+        self.prefix = (Kp, Vp, prefix_len, group_start)  # kept alive with the descriptor
+        _same_device(dev, Kp=Kp, Vp=Vp, prefix_len=prefix_len, group_start=group_start)
+        self.out = torch.empty(B, Hq, D, dtype=out_dtype, device=dev)
+        self.lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+        self.q = torch.empty(B, Hq, D, dtype=dt, device=dev)  # the turned queries of step
+        self.k = torch.empty(B, Hkv, D, dtype=dt, device=dev)
+        with torch.cuda.device(dev):
+            nbytes = csa.csa_prefix_decode_workspace_bytes(dt, B, Hq, Hkv, D, N, Tp, T, accumulate)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        self.desc = csa.prefix_decode_desc(
+            dtype=dt, B=B, Hq=Hq, Hkv=Hkv, D=D, scale=1.0 / math.sqrt(D) if scale is None else scale,
+            N=N, Tp=Tp, T=T, K=cache.K, V=cache.V, k_stride=cache.k_stride, v_stride=cache.v_stride,
+            len=cache.lengths, out=self.out, out_dtype=out_dtype, lse_out=self.lse,
+            weights=cache.weights if accumulate else None, decay=decay, workspace=self.workspace,
+            workspace_bytes=nbytes, **kw)
+
+    def attend(self, q: torch.Tensor, stream=None):
+        """Attention of q [B, Hq, D] over the prefixes and the cache as they
+        are; returns (out, lse), this decoder's buffers."""
+        _dense("q", q, self.cache.K.dtype, self.out.shape)
+        self.desc.q = q.data_ptr()
+        csa.csa_prefix_decode(self.desc, stream=stream)
+        return self.out, self.lse
+
+    def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None):
+        """One decode step: q [B, Hq, D] and k [B, Hkv, D] are turned to the next
+        position (when there is a rotary), k and v enter the cache, and q attends."""
+        c = self.cache
+        if self.rotary is not None:
+            self.rotary.rotate(q[:, None], k[:, None], positions=c.next_pos[:, None],
+                               q_out=self.q[:, None], k_out=self.k[:, None], stream=stream)
+            q, k = self.q, self.k
+        c.insert(k, v, stream=stream)
+        return self.attend(q, stream=stream)
