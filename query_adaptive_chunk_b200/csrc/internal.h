@@ -221,4 +221,10 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64
                        uint64_t row_stride, uint32_t box_rows, uint32_t box_cols,
                        std::string* why);
 
+// The same over a tensor [n2, n1, rows, cols] with element strides s2, s1 and
+// row_stride (any order); box [1, 1, box_rows, box_cols].
+bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                       uint64_t n1, uint64_t n2, uint64_t row_stride, uint64_t s1, uint64_t s2,
+                       uint32_t box_rows, uint32_t box_cols, std::string* why);
+
 }  // namespace csa

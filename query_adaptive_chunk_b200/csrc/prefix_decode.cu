@@ -14,31 +14,10 @@
 #include <algorithm>
 #include <cmath>
 
-#include "prefix_work.cuh"
+#include "prefix_decode.cuh"
 
 namespace csa {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct PdParams {
-  PdShape s;
-  const void *q, *Kp, *Vp, *K, *V;
-  int64_t kps[3], vps[3], ks[3], vs[3];  // strides in elements: prefix / sequence, head, token
-  int Hq;
-  float scale_log2;
-  // workspace
-  int32_t *starts, *ubase, *gsan;
-  float *plse, *po, *olse, *oo, *logits;
-  int64_t Tl;  // logits' row length
-  // outputs
-  void* out;
-  int out_bf16;
-  float* lse_out;
-  float* acc;
-  float decay;
-};
 
 // ------------------------------------------------------------------ fp32
 //
@@ -48,15 +27,9 @@ constexpr int kF32Rows = 32;
 constexpr int kF32Threads = 256;
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kF32Threads) attend_simple_kernel(const PdParams p) {
+template <int D>
+__global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams p) {
   constexpr int KS = D + 4, SS = kPdChunk + 4;
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;                           // [32][KS]
@@ -80,15 +53,15 @@ __global__ void __launch_bounds__(kF32Threads) attend_simple_kernel(const PdPara
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < g.rows) {
         const int row = g.row0 + r, b = row / p.s.G, hd = g.h * p.s.G + row % p.s.G;
-        x = ld4(static_cast<const T*>(p.q) + (static_cast<int64_t>(b) * p.Hq + hd) * D + d);
+        x = ld4(static_cast<const float*>(p.q) + (static_cast<int64_t>(b) * p.Hq + hd) * D + d);
       }
       *reinterpret_cast<float4*>(sq + r * KS + d) = x;
     }
     const int64_t* kst = g.own ? p.ks : p.kps;
     const int64_t* vst = g.own ? p.vs : p.vps;
     const int64_t k0 = g.own ? g.b : g.n;
-    const T* Kg = static_cast<const T*>(g.own ? p.K : p.Kp) + k0 * kst[0] + g.h * kst[1];
-    const T* Vg = static_cast<const T*>(g.own ? p.V : p.Vp) + k0 * vst[0] + g.h * vst[1];
+    const float* Kg = static_cast<const float*>(g.own ? p.K : p.Kp) + k0 * kst[0] + g.h * kst[1];
+    const float* Vg = static_cast<const float*>(g.own ? p.V : p.Vp) + k0 * vst[0] + g.h * vst[1];
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[2][D / 16];
 #pragma unroll
@@ -206,12 +179,20 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeKeys = 1024;
 constexpr int kMaxG = 16;
 
-// Partials of one query head: `np` CTAs of its prefix unit, then `no` of its
-// own unit.
+// Partials of one query head: `np` of its prefix unit, then `no` of its own
+// unit.  Partial i lies at row (i >> sh) * step + (i & sh) * half from the
+// unit's first: sh = 1 where a CTA's share is in two halves.
 struct MergeSrc {
   const float *pl, *po, *ol, *oo;
   int np, no;
-  int pstep, ostep;  // floats between the lse of two CTAs' slots
+  int psh, pstep, phalf;
+  int osh, ostep, ohalf;
+  __device__ __forceinline__ int64_t prow(int i) const {
+    return static_cast<int64_t>(i >> psh) * pstep + (i & psh) * phalf;
+  }
+  __device__ __forceinline__ int64_t orow(int i) const {
+    return static_cast<int64_t>(i >> osh) * ostep + (i & osh) * ohalf;
+  }
 };
 
 template <int D>
@@ -243,10 +224,13 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p) 
         const int ui = h * tiles + tile, x = p.starts[n] + ui * c;
         const int c0 = pd_cta_of(x, W, s.P), c1 = pd_cta_of(x + c - 1, W, s.P);
         const int64_t slot = static_cast<int64_t>(c0) + p.ubase[n] + ui;
-        m.np = c1 - c0 + 1;
+        const bool split = p.halves == 2 && min(s.R, seqs * s.G - tile * s.R) <= s.R / 2;
+        m.psh = split ? 1 : 0;
+        m.np = (c1 - c0 + 1) << m.psh;
         m.pl = p.plse + slot * s.R + r;
         m.po = p.po + (slot * s.R + r) * D;
         m.pstep = s.R;
+        m.phalf = s.R / 2;
       }
     }
     const int c = pd_chunks(len);
@@ -254,15 +238,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p) 
       const int x = p.starts[s.N + b] + h * c;
       const int c0 = pd_cta_of(x, W, s.P), c1 = pd_cta_of(x + c - 1, W, s.P);
       const int64_t slot = static_cast<int64_t>(c0) + u;
-      m.no = c1 - c0 + 1;
-      m.ol = p.olse + slot * s.G + g;
-      m.oo = p.oo + (slot * s.G + g) * D;
-      m.ostep = s.G;
+      m.osh = p.halves - 1;
+      m.no = (c1 - c0 + 1) << m.osh;
+      m.ostep = p.halves * s.G;
+      m.ohalf = s.G;
+      m.ol = p.olse + slot * m.ostep + g;
+      m.oo = p.oo + (slot * m.ostep + g) * D;
     }
     const int ns = m.np + m.no;
     auto lse_at = [&](int i) -> float {
-      return i < m.np ? m.pl[static_cast<int64_t>(i) * m.pstep]
-                      : m.ol[static_cast<int64_t>(i - m.np) * m.ostep];
+      return i < m.np ? m.pl[m.prow(i)] : m.ol[m.orow(i - m.np)];
     };
     float mx = -INFINITY;
     for (int i = lane; i < ns; i += 32) mx = fmaxf(mx, lse_at(i));
@@ -293,8 +278,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p) 
         const int ns = L == -INFINITY ? 0 : m.np + m.no;
         for (int i = part; i < ns; i += parts) {
           const bool pre = i < m.np;
-          const int64_t k = pre ? static_cast<int64_t>(i) * m.pstep
-                                : static_cast<int64_t>(i - m.np) * m.ostep;
+          const int64_t k = pre ? m.prow(i) : m.orow(i - m.np);
           const float ls = pre ? m.pl[k] : m.ol[k];
           if (ls == -INFINITY) continue;  // this slot's row was not written
           const float w = exp2f(ls - L);
@@ -331,7 +315,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p) 
       }
     }
     if (p.lse_out && tid < s.G)
-      p.lse_out[static_cast<int64_t>(b) * p.Hq + h * s.G + tid] = lse2[tid] * kLn2;
+      p.lse_out[static_cast<int64_t>(b) * p.Hq + h * s.G + tid] = lse2[tid] * kPdLn2;
   }
   if (p.acc != nullptr) {
     const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kMergeKeys;
@@ -352,14 +336,11 @@ struct PdLayout {
   int64_t Tl;
 };
 
-int pd_parts(bool bf16, int num_sms) {
-  (void)bf16;
-  return 2 * num_sms;
-}
-int pd_rows(bool bf16) {
-  (void)bf16;
-  return kF32Rows;
-}
+// CTAs that share the chunks: one per SM for bf16 (it takes the SM's whole
+// shared memory), two for fp32.
+int pd_parts(bool bf16, int num_sms) { return bf16 ? num_sms : 2 * num_sms; }
+int pd_rows(bool bf16) { return bf16 ? pd_tc_rows() : kF32Rows; }
+int pd_halves(bool bf16) { return bf16 ? 2 : 1; }
 
 PdLayout pd_layout(bool bf16, int B, int Hkv, int G, int D, int N, int64_t T, bool weights, int P) {
   const int64_t R = pd_rows(bf16), U = static_cast<int64_t>(B) * Hkv;
@@ -378,20 +359,20 @@ PdLayout pd_layout(bool bf16, int B, int Hkv, int G, int D, int N, int64_t T, bo
   w.gsan = take(4ll * (N + 1));
   w.plse = take(4 * pslots * R);
   w.po = take(4 * pslots * R * D);
-  w.olse = take(4 * oslots * G);
-  w.oo = take(4 * oslots * G * D);
+  w.olse = take(4 * oslots * pd_halves(bf16) * G);
+  w.oo = take(4 * oslots * pd_halves(bf16) * G * D);
   w.logits = take(weights ? 4 * U * G * w.Tl : 0);
   w.total = at;
   return w;
 }
 
-template <typename T, int D>
-cudaError_t launch_simple(const Launch& l, const PdParams& p) {
+template <int D>
+cudaError_t launch_attend_f32(const Launch& l, const PdParams& p) {
   const int smem = ((kF32Rows + kPdChunk) * (D + 4) + kPdChunk * D + kF32Rows * (kPdChunk + 4)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(attend_simple_kernel<T, D>,
+  cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attend_simple_kernel<T, D><<<p.s.P, kF32Threads, smem, l.stream>>>(p);
+  attend_f32_kernel<D><<<p.s.P, kF32Threads, smem, l.stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -419,7 +400,6 @@ int64_t prefix_decode_workspace_bytes(bool bf16, int B, int Hkv, int G, int D, i
 }
 
 cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std::string* why) {
-  (void)why;
   const int G = a.Hq / a.Hkv, P = pd_parts(a.bf16, l.num_sms);
   const PdLayout w = pd_layout(a.bf16, a.B, a.Hkv, G, a.D, a.N, a.T, a.weights != nullptr, P);
   char* ws = static_cast<char*>(a.workspace);
@@ -438,7 +418,8 @@ cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std
     p.vs[i] = a.vs[i];
   }
   p.Hq = a.Hq;
-  p.scale_log2 = a.scale * kLog2e;
+  p.halves = pd_halves(a.bf16);
+  p.scale_log2 = a.scale * kPdLog2e;
   p.starts = reinterpret_cast<int32_t*>(ws + w.starts);
   p.ubase = reinterpret_cast<int32_t*>(ws + w.ubase);
   p.gsan = reinterpret_cast<int32_t*>(ws + w.gsan);
@@ -455,9 +436,9 @@ cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std
   p.decay = a.decay;
   cudaError_t e;
   if (a.bf16)
-    e = a.D == 128 ? launch_simple<__nv_bfloat16, 128>(l, p) : launch_simple<__nv_bfloat16, 64>(l, p);
+    e = launch_attend_tc(l, p, a.D, why);
   else
-    e = a.D == 128 ? launch_simple<float, 128>(l, p) : launch_simple<float, 64>(l, p);
+    e = a.D == 128 ? launch_attend_f32<128>(l, p) : launch_attend_f32<64>(l, p);
   if (e != cudaSuccess) return e;
   return a.D == 128 ? launch_pd_merge<128>(l, p) : launch_pd_merge<64>(l, p);
 }

@@ -45,4 +45,26 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64
   return true;
 }
 
+bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                       uint64_t n1, uint64_t n2, uint64_t row_stride, uint64_t s1, uint64_t s2,
+                       uint32_t box_rows, uint32_t box_cols, std::string* why) {
+  auto fn = encode_fn();
+  if (fn == nullptr) {
+    if (why) *why = "cuTensorMapEncodeTiled is not available from the driver";
+    return false;
+  }
+  cuuint64_t gdim[4] = {cols, rows, n1, n2};
+  cuuint64_t gstride[3] = {row_stride * 2, s1 * 2, s2 * 2};
+  cuuint32_t box[4] = {box_cols, box_rows, 1, 1};
+  cuuint32_t estride[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gdim, gstride,
+                  box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    if (why) *why = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(static_cast<int>(r));
+    return false;
+  }
+  return true;
+}
+
 }  // namespace csa
