@@ -41,10 +41,9 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
   __shared__ int scan_sh[33];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   if (tid < 32) pd_groups(p.s, gs);
+  const int key0 = tid < p.s.N + p.s.B ? pd_item_keys(p.s, tid) : 0;
   __syncthreads();
-  const bool plan = blockIdx.x == 0;
-  pd_locate(p.s, gs, blockIdx.x, &st, scan_sh, plan ? p.starts : nullptr, plan ? p.ubase : nullptr);
-  if (plan && tid <= p.s.N) p.gsan[tid] = gs[tid];
+  pd_locate(p.s, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.plan : nullptr);
   PdWalk walk(p.s, gs, st);
   PdSeg g;
   while (walk.next(g)) {
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
       }
     }
     const int64_t slot = static_cast<int64_t>(blockIdx.x) + g.unit;
-    const int rows = g.own ? p.s.G : p.s.R;
+    const int rows = g.own ? p.s.G : p.slot_rows;
     float* po = (g.own ? p.oo : p.po) + slot * rows * D;
     float* pl = (g.own ? p.olse : p.plse) + slot * rows;
 #pragma unroll
@@ -171,13 +170,16 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
 
 // ------------------------------------------------------------------ merge
 //
-// A CTA joins the partials of one (sequence, KV head) and, block by block of
-// kMergeKeys own keys, adds the keys' weights; the first block's CTA writes
-// the output.  Reads the partials once (they sit in L2) and 4 bytes per head
-// and own key; bound by latency at the usual sizes.
+// A CTA joins the partials of one (sequence, KV head) and adds the weights of
+// a share of its own keys; the first share's CTA writes the output.  Reads the
+// partials once (they sit in L2) and 4 bytes per head and own key.  Bound by
+// latency at the usual sizes, so each step's loads go out together: where the
+// partials lie, their lse, then their rows and the logits.  The shares are as
+// many as keep every SM busy with a few CTAs each.
 constexpr int kMergeThreads = 256;
-constexpr int kMergeKeys = 1024;
+constexpr int kMergeMinKeys = 1024;  // own keys per share at least
 constexpr int kMaxG = 16;
+constexpr int kMergeSrcs = 64;       // partials per head whose factors are kept
 
 // Partials of one query head: `np` of its prefix unit, then `no` of its own
 // unit.  Partial i lies at row (i >> sh) * step + (i & sh) * half from the
@@ -193,73 +195,84 @@ struct MergeSrc {
   __device__ __forceinline__ int64_t orow(int i) const {
     return static_cast<int64_t>(i >> osh) * ostep + (i & osh) * ohalf;
   }
+  __device__ __forceinline__ float lse(int i) const {
+    return i < np ? pl[prow(i)] : ol[orow(i - np)];
+  }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's partials
-  __shared__ float lse2[kMaxG];
-  __shared__ MergeSrc src[kMaxG];
-  __shared__ float4 red[kMergeThreads];
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, int share) {
   const PdShape& s = p.s;
   const int u = blockIdx.y, b = u / s.Hkv, h = u - b * s.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int W = p.starts[s.N + s.B];
   const int len = pd_own_len(s, b);
+  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * share;
+  if (blockIdx.x > 0 && k0 >= len) return;
+  __shared__ float lse2[kMaxG];
+  __shared__ MergeSrc src[kMaxG];
+  __shared__ float fac[kMaxG][kMergeSrcs];
+  __shared__ float4 red[kMergeThreads];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's partials
   for (int g = warp; g < s.G; g += kMergeThreads / 32) {
     MergeSrc m{};
-    // the sequence's group
-    int n = -1;
-    for (int i0 = 0; i0 < s.N; i0 += 32) {
-      const int i = i0 + lane;
-      const unsigned hit =
-          __ballot_sync(0xffffffffu, i < s.N && p.gsan[i] <= b && b < p.gsan[i + 1]);
-      if (hit) n = i0 + __ffs(hit) - 1;
-    }
+    const int W = p.plan.starts[s.N + s.B], x_own = p.plan.starts[s.N + b];
+    const int n = s.N > 0 ? p.plan.group[b] : -1;
     if (n >= 0) {
-      const int seqs = p.gsan[n + 1] - p.gsan[n], tiles = pd_tiles(s, seqs);
+      const int g0 = p.plan.gsan[n], g1 = p.plan.gsan[n + 1];
+      const int x_pre = p.plan.starts[n], ub = p.plan.ubase[n];
       const int c = pd_chunks(pd_prefix_len(s, n));
       if (c > 0) {
-        const int row = (b - p.gsan[n]) * s.G + g, tile = row / s.R, r = row - tile * s.R;
-        const int ui = h * tiles + tile, x = p.starts[n] + ui * c;
+        const int seqs = g1 - g0, tiles = pd_tiles(s, seqs);
+        int r = (b - g0) * s.G + g;
+        const int tile = r / s.R;
+        r -= tile * s.R;
+        const int rows = min(s.R, seqs * s.G - tile * s.R);
+        const int ui = h * tiles + tile, x = x_pre + ui * c;
         const int c0 = pd_cta_of(x, W, s.P), c1 = pd_cta_of(x + c - 1, W, s.P);
-        const int64_t slot = static_cast<int64_t>(c0) + p.ubase[n] + ui;
-        const bool split = p.halves == 2 && min(s.R, seqs * s.G - tile * s.R) <= s.R / 2;
-        m.psh = split ? 1 : 0;
+        if (p.halves == 2) {
+          const int rh = s.R / 2;
+          m.psh = rows <= rh ? 1 : 0;
+          if (r >= rh) r += p.slot_rows / 2 - rh;
+        }
+        const int64_t row = (static_cast<int64_t>(c0) + ub + ui) * p.slot_rows + r;
         m.np = (c1 - c0 + 1) << m.psh;
-        m.pl = p.plse + slot * s.R + r;
-        m.po = p.po + (slot * s.R + r) * D;
-        m.pstep = s.R;
-        m.phalf = s.R / 2;
+        m.pl = p.plse + row;
+        m.po = p.po + row * D;
+        m.pstep = p.slot_rows;
+        m.phalf = p.slot_rows / 2;
       }
     }
     const int c = pd_chunks(len);
     if (c > 0) {
-      const int x = p.starts[s.N + b] + h * c;
+      const int x = x_own + h * c;
       const int c0 = pd_cta_of(x, W, s.P), c1 = pd_cta_of(x + c - 1, W, s.P);
-      const int64_t slot = static_cast<int64_t>(c0) + u;
       m.osh = p.halves - 1;
       m.no = (c1 - c0 + 1) << m.osh;
       m.ostep = p.halves * s.G;
       m.ohalf = s.G;
-      m.ol = p.olse + slot * m.ostep + g;
-      m.oo = p.oo + (slot * m.ostep + g) * D;
+      const int64_t row = (static_cast<int64_t>(c0) + u) * m.ostep + g;
+      m.ol = p.olse + row;
+      m.oo = p.oo + row * D;
     }
     const int ns = m.np + m.no;
-    auto lse_at = [&](int i) -> float {
-      return i < m.np ? m.pl[m.prow(i)] : m.ol[m.orow(i - m.np)];
-    };
-    float mx = -INFINITY;
-    for (int i = lane; i < ns; i += 32) mx = fmaxf(mx, lse_at(i));
+    // the first two rounds (64 partials) stay in registers
+    float l0 = lane < ns ? m.lse(lane) : -INFINITY;
+    float l1 = lane + 32 < ns ? m.lse(lane + 32) : -INFINITY;
+    float mx = fmaxf(l0, l1);
+    for (int i = lane + 64; i < ns; i += 32) mx = fmaxf(mx, m.lse(i));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float base = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
-    for (int i = lane; i < ns; i += 32) sum += exp2f(lse_at(i) - base);
+    float sum = exp2f(l0 - base) + exp2f(l1 - base);
+    for (int i = lane + 64; i < ns; i += 32) sum += exp2f(m.lse(i) - base);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float L = sum == 0.f ? -INFINITY : base + log2f(sum);
+    // a partial's share of the sum; 0 where its row was not written
+    fac[g][lane] = l0 == -INFINITY ? 0.f : exp2f(l0 - L);
+    fac[g][lane + 32] = l1 == -INFINITY ? 0.f : exp2f(l1 - L);
     if (lane == 0) {
-      lse2[g] = sum == 0.f ? -INFINITY : base + log2f(sum);
+      lse2[g] = L;
       src[g] = m;
     }
   }
@@ -273,20 +286,35 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p) 
       const int g = task / D4, d = (task % D4) * 4;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (task < tasks && part < parts) {
-        const MergeSrc& m = src[g];
+        const MergeSrc m = src[g];
         const float L = lse2[g];
         const int ns = L == -INFINITY ? 0 : m.np + m.no;
-        for (int i = part; i < ns; i += parts) {
-          const bool pre = i < m.np;
-          const int64_t k = pre ? m.prow(i) : m.orow(i - m.np);
-          const float ls = pre ? m.pl[k] : m.ol[k];
-          if (ls == -INFINITY) continue;  // this slot's row was not written
-          const float w = exp2f(ls - L);
-          const float4 v = ld4((pre ? m.po : m.oo) + k * D + d);
+        auto row = [&](int i) -> const float* {
+          return i < m.np ? m.po + m.prow(i) * D + d : m.oo + m.orow(i - m.np) * D + d;
+        };
+        auto add = [&](float w, const float4& v) {
           o.x += w * v.x;
           o.y += w * v.y;
           o.z += w * v.z;
           o.w += w * v.w;
+        };
+        const int nf = min(ns, kMergeSrcs);
+        for (int i = part; i < nf; i += 4 * parts) {  // four rows in flight
+          float w[4];
+          float4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = i + k * parts;
+            w[k] = j < nf ? fac[g][j] : 0.f;
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w[k] != 0.f) v[k] = ld4(row(j));  // (a NaN factor too)
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) add(w[k], v[k]);
+        }
+        for (int i = kMergeSrcs + part; i < ns; i += parts) {
+          const float l = m.lse(i);
+          if (l != -INFINITY) add(exp2f(l - L), ld4(row(i)));
         }
       }
       if (parts > 1) {
@@ -318,32 +346,45 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p) 
       p.lse_out[static_cast<int64_t>(b) * p.Hq + h * s.G + tid] = lse2[tid] * kPdLn2;
   }
   if (p.acc != nullptr) {
-    const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kMergeKeys;
     float* acc = p.acc + static_cast<int64_t>(u) * s.T;
     const float* lg = p.logits + static_cast<int64_t>(u) * s.G * p.Tl;
-    for (int64_t j = k0 + tid; j < min(k0 + kMergeKeys, static_cast<int64_t>(len));
-         j += kMergeThreads) {
-      float w = 0.f;
-      for (int g = 0; g < s.G; ++g)
-        if (lse2[g] != -INFINITY) w += exp2f(lg[g * p.Tl + j] - lse2[g]);
-      acc[j] = p.decay == 0.f ? w : p.decay * acc[j] + w;
+    const int64_t k1 = min(k0 + share, static_cast<int64_t>(len));
+    // four keys a thread: the logits' rows start on 16 bytes, the sums' need not
+    for (int64_t j = k0 + 4 * tid; j < k1; j += 4 * kMergeThreads) {
+      float w[4] = {0.f, 0.f, 0.f, 0.f}, old[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) old[i] = p.decay != 0.f && j + i < k1 ? acc[j + i] : 0.f;
+      for (int g = 0; g < s.G; ++g) {
+        const float L = lse2[g];
+        const float4 x = ld4(lg + g * p.Tl + j);
+        if (L != -INFINITY) {
+          w[0] += fast_exp2(x.x - L);
+          w[1] += fast_exp2(x.y - L);
+          w[2] += fast_exp2(x.z - L);
+          w[3] += fast_exp2(x.w - L);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j + i < k1) acc[j + i] = p.decay != 0.f ? p.decay * old[i] + w[i] : w[i];
     }
   }
 }
 
 struct PdLayout {
-  int64_t starts, ubase, gsan, plse, po, olse, oo, logits, total;
-  int64_t Tl;
+  int64_t starts, ubase, gsan, group, plse, po, olse, oo, logits, total;
+  int64_t Tl, slots;
 };
 
 // CTAs that share the chunks: one per SM for bf16 (it takes the SM's whole
 // shared memory), two for fp32.
 int pd_parts(bool bf16, int num_sms) { return bf16 ? num_sms : 2 * num_sms; }
-int pd_rows(bool bf16) { return bf16 ? pd_tc_rows() : kF32Rows; }
+int pd_rows(bool bf16, int G) { return bf16 ? pd_tc_rows(G) : kF32Rows; }
+int pd_slot_rows(bool bf16) { return bf16 ? kPdTcSlotRows : kF32Rows; }
 int pd_halves(bool bf16) { return bf16 ? 2 : 1; }
 
 PdLayout pd_layout(bool bf16, int B, int Hkv, int G, int D, int N, int64_t T, bool weights, int P) {
-  const int64_t R = pd_rows(bf16), U = static_cast<int64_t>(B) * Hkv;
+  const int64_t R = pd_rows(bf16, G), SR = pd_slot_rows(bf16), U = static_cast<int64_t>(B) * Hkv;
   const int64_t pslots = N > 0 ? P + Hkv * (static_cast<int64_t>(B) * G / R + N) : 0;
   const int64_t oslots = T > 0 ? P + U : 0;
   PdLayout w{};
@@ -357,8 +398,10 @@ PdLayout pd_layout(bool bf16, int B, int Hkv, int G, int D, int N, int64_t T, bo
   w.starts = take(4ll * (N + B + 1));
   w.ubase = take(4ll * (N + 1));
   w.gsan = take(4ll * (N + 1));
-  w.plse = take(4 * pslots * R);
-  w.po = take(4 * pslots * R * D);
+  w.group = take(4ll * B);
+  w.slots = pslots;
+  w.plse = take(4 * pslots * SR);
+  w.po = take(4 * pslots * SR * D);
   w.olse = take(4 * oslots * pd_halves(bf16) * G);
   w.oo = take(4 * oslots * pd_halves(bf16) * G * D);
   w.logits = take(weights ? 4 * U * G * w.Tl : 0);
@@ -379,9 +422,14 @@ cudaError_t launch_attend_f32(const Launch& l, const PdParams& p) {
 template <int D>
 cudaError_t launch_pd_merge(const Launch& l, const PdParams& p) {
   cudaLaunchConfig_t cfg = {};
-  const int64_t blocks =
-      p.acc ? std::max<int64_t>(1, (p.s.T + kMergeKeys - 1) / kMergeKeys) : 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.s.B * p.s.Hkv));
+  const int64_t U = static_cast<int64_t>(p.s.B) * p.s.Hkv;
+  int64_t blocks = 1;
+  if (p.acc)  // about four CTAs per SM, of at least kMergeMinKeys keys
+    blocks = std::max<int64_t>(1, std::min<int64_t>((p.s.T + kMergeMinKeys - 1) / kMergeMinKeys,
+                                                    4ll * l.num_sms / U));
+  int64_t share = (p.s.T + blocks - 1) / blocks;
+  share = std::max<int64_t>(4, (share + 3) / 4 * 4);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(U));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = l.stream;
   cudaLaunchAttribute attr[1];
@@ -389,7 +437,7 @@ cudaError_t launch_pd_merge(const Launch& l, const PdParams& p) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p, static_cast<int>(share));
 }
 
 }  // namespace
@@ -404,7 +452,7 @@ cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std
   const PdLayout w = pd_layout(a.bf16, a.B, a.Hkv, G, a.D, a.N, a.T, a.weights != nullptr, P);
   char* ws = static_cast<char*>(a.workspace);
   PdParams p{};
-  p.s = PdShape{a.B,  a.Hkv, G,            a.N,           pd_rows(a.bf16), P,
+  p.s = PdShape{a.B,  a.Hkv, G,            a.N,           pd_rows(a.bf16, G), P,
                 a.Tp, a.T,   a.prefix_len, a.group_start, a.len,           l.err};
   p.q = a.q;
   p.Kp = a.Kp;
@@ -420,9 +468,10 @@ cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std
   p.Hq = a.Hq;
   p.halves = pd_halves(a.bf16);
   p.scale_log2 = a.scale * kPdLog2e;
-  p.starts = reinterpret_cast<int32_t*>(ws + w.starts);
-  p.ubase = reinterpret_cast<int32_t*>(ws + w.ubase);
-  p.gsan = reinterpret_cast<int32_t*>(ws + w.gsan);
+  p.slot_rows = pd_slot_rows(a.bf16);
+  p.slots = w.slots;
+  p.plan = PdPlan{reinterpret_cast<int32_t*>(ws + w.starts), reinterpret_cast<int32_t*>(ws + w.ubase),
+                  reinterpret_cast<int32_t*>(ws + w.gsan), reinterpret_cast<int32_t*>(ws + w.group)};
   p.plse = reinterpret_cast<float*>(ws + w.plse);
   p.po = reinterpret_cast<float*>(ws + w.po);
   p.olse = reinterpret_cast<float*>(ws + w.olse);

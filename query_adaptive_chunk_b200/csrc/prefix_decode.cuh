@@ -14,12 +14,14 @@ struct PdParams {
   int64_t kps[3], vps[3], ks[3], vs[3];  // strides in elements: prefix / sequence, head, token
   int Hq;
   float scale_log2;
-  // workspace.  A prefix unit's slot holds R rows, an own unit's `halves` * G
-  // rows: with halves = 2 a unit of at most R / 2 rows may be split once more
-  // inside its CTA, even chunks in the first half of the slot's rows, odd
-  // chunks in the second.
-  int halves;
-  int32_t *starts, *ubase, *gsan;
+  // workspace.  A prefix unit's slot holds `slot_rows` rows, an own unit's
+  // `halves` * G.  With halves = 2 row r of a tile lies at (r / (R/2)) *
+  // slot_rows/2 + r % (R/2), and a unit of at most R / 2 rows (an own one always)
+  // is split once more inside its CTA: even chunks' rows in the slot's first
+  // half, odd chunks' in its second.
+  int halves, slot_rows;
+  int64_t slots;  // prefix slots
+  PdPlan plan;
   float *plse, *po, *olse, *oo, *logits;
   int64_t Tl;  // logits' row length
   // outputs
@@ -31,7 +33,8 @@ struct PdParams {
 };
 
 // prefix_decode_tc.cu: the bf16 attention kernel.
-int pd_tc_rows();
+int pd_tc_rows(int G);           // query rows per tile
+constexpr int kPdTcSlotRows = 256;
 cudaError_t launch_attend_tc(const Launch& l, const PdParams& p, int D, std::string* why);
 
 }  // namespace csa

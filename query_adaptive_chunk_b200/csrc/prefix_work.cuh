@@ -6,12 +6,13 @@
 //     group n (row = sequence * G + head of the group) against prefix n;
 //   own units (b, h): the G query heads of one sequence against its own cache.
 // A unit's keys are cut into chunks of kPdChunk.  All chunks of all units lie
-// end to end (prefixes first; within a prefix by head, then row tile) and CTA
-// c of P = min(CTAs, W) takes chunks [W c / P, W (c + 1) / P): every SM streams the same
-// number of keys whatever the lengths.  A CTA that holds any of unit i's
-// chunks writes one partial (normalised rows and their log2-sum-exp) to slot
-// c + i: the pairs (c, i) met along the line grow by one in c or in i at a
-// time, so slots are distinct and number at most P + units.
+// end to end (prefixes first; within a prefix by head, then row tile; own units by
+// sequence, then head) and CTA c of P = min(CTAs, W) takes chunks [W c / P,
+// W (c + 1) / P): every SM streams the same number of keys whatever the
+// lengths.  A CTA that holds any of unit i's chunks writes one partial
+// (normalised rows and their log2-sum-exp) to slot c + i: the pairs (c, i) met
+// along the line grow by one in c or in i at a time, so slots are distinct
+// and number at most P + units.
 #pragma once
 
 #include "internal.h"
@@ -46,6 +47,10 @@ __device__ __forceinline__ int pd_own_len(const PdShape& s, int b) {
   if (s.T == 0) return 0;
   return s.len ? pd_clamp(__ldg(s.len + b), s.T, s.err) : static_cast<int>(s.T);
 }
+// Keys of item i: prefix i, or the own cache of sequence i - N.
+__device__ __forceinline__ int pd_item_keys(const PdShape& s, int i) {
+  return i < s.N ? pd_prefix_len(s, i) : pd_own_len(s, i - s.N);
+}
 __device__ __forceinline__ int pd_chunks(int keys) { return (keys + kPdChunk - 1) / kPdChunk; }
 __device__ __forceinline__ int pd_tiles(const PdShape& s, int seqs) {
   return (seqs * s.G + s.R - 1) / s.R;
@@ -79,63 +84,93 @@ __device__ __forceinline__ void pd_groups(const PdShape& s, int* gs) {
   }
 }
 
-// A CTA's place on the line.  `item` < N: prefix item; else sequence item - N.
+// A CTA's place on the line.
 struct PdStart {
-  int total;       // W
-  int x0, x1;      // this CTA's chunks
-  int item, off;   // the item holding x0 and x0's offset in it
-  int units;       // prefix units in all
-  int unit0;       // prefix units before `item` (prefix items only)
+  int left;             // its chunks
+  int item, h, tile, j; // where they start: item, head, row tile, chunk of the unit
+  int unit0;            // prefix units before `item` (prefix items only)
 };
 
-// Block-wide: fills *st (shared).  `gs` is shared, filled by pd_groups.
-// starts (global, optional): for every item its first chunk, then W;
-// ubase (global, optional): for every prefix its first unit, then the count.
-__device__ __forceinline__ void pd_locate(const PdShape& s, const int* gs, int cta, PdStart* st,
-                                          int* scan_sh, int32_t* starts, int32_t* ubase) {
+// What the merge needs to find a unit's partials, written by one CTA.
+struct PdPlan {
+  int32_t* starts;  // [N + B + 1] first chunk of each item, then W
+  int32_t* ubase;   // [N + 1] first unit of each prefix
+  int32_t* gsan;    // [N + 1] the sanitised group bounds
+  int32_t* group;   // [B] each sequence's prefix, or -1
+};
+
+// Block-wide: fills *st (shared).  `gs` (shared) is filled by pd_groups in the
+// calling code before a barrier; key0 = pd_item_keys of item threadIdx.x,
+// loaded before that barrier (any value for threads past the items).
+__device__ __forceinline__ void pd_locate(const PdShape& s, const int* gs, int key0, PdStart* st,
+                                          int* scan_sh, const PdPlan* plan) {
   const int items = s.N + s.B, nt = blockDim.x, tid = threadIdx.x;
-  auto weight = [&](int i) -> int {
-    if (i < s.N) return pd_tiles(s, gs[i + 1] - gs[i]) * s.Hkv * pd_chunks(pd_prefix_len(s, i));
-    return i < items ? s.Hkv * pd_chunks(pd_own_len(s, i - s.N)) : 0;
+  auto units = [&](int i) -> int {
+    return i < s.N ? pd_tiles(s, gs[i + 1] - gs[i]) * s.Hkv : s.Hkv;
   };
-  int run = 0;
-  for (int i0 = 0; i0 < items; i0 += nt) {
-    const int i = i0 + tid;
-    int tot;
-    const int ex = block_exclusive_scan(weight(i), scan_sh, &tot);
-    if (starts && i < items) starts[i] = run + ex;
-    run += tot;
-  }
-  if (tid == 0) {
-    st->total = run;
-    // at least one chunk per CTA that takes part: each writes the slots it owns
-    const int P = max(1, min(s.P, run));
-    st->x0 = cta < P ? static_cast<int>(static_cast<int64_t>(run) * cta / P) : run;
-    st->x1 = cta < P ? static_cast<int>(static_cast<int64_t>(run) * (cta + 1) / P) : run;
-    if (starts) starts[items] = run;
-    int u = 0;
-    for (int n = 0; n < s.N; ++n) {
-      if (ubase) ubase[n] = u;
-      u += pd_tiles(s, gs[n + 1] - gs[n]) * s.Hkv;
+  auto place = [&](int i, int u, int c, int off, int take) {  // one thread: CTA starts in item i
+    st->left = take;
+    st->item = i;
+    const int ui = off / c, tiles = i < s.N ? u / s.Hkv : 1;
+    st->h = ui / tiles;
+    st->tile = ui - st->h * tiles;
+    st->j = off - ui * c;
+    int before = 0;
+    for (int n = 0; n < min(i, s.N); ++n) before += units(n);
+    st->unit0 = before;
+  };
+  auto share = [&](int W, int* x0, int* x1) {
+    // at least one chunk for each CTA that takes part: each writes the slots it owns
+    const int P = max(1, min(s.P, W)), c = static_cast<int>(blockIdx.x);
+    *x0 = c < P ? static_cast<int>(static_cast<int64_t>(W) * c / P) : W;
+    *x1 = c < P ? static_cast<int>(static_cast<int64_t>(W) * (c + 1) / P) : W;
+  };
+  if (tid == 0) st->left = 0;
+  int W, x0, x1;
+  if (items <= nt) {
+    const int u = tid < items ? units(tid) : 0, c = tid < items ? pd_chunks(key0) : 0;
+    const int ex = block_exclusive_scan(u * c, scan_sh, &W);
+    share(W, &x0, &x1);
+    if (x0 >= ex && x0 < ex + u * c) place(tid, u, c, x0 - ex, x1 - x0);  // at most one item
+    if (plan && tid < items) plan->starts[tid] = ex;
+  } else {
+    W = 0;
+    for (int i0 = 0; i0 < items; i0 += nt) {
+      const int i = i0 + tid;
+      int tot;
+      const int ex = block_exclusive_scan(i < items ? units(i) * pd_chunks(pd_item_keys(s, i)) : 0,
+                                          scan_sh, &tot);
+      if (plan && i < items) plan->starts[i] = W + ex;
+      W += tot;
     }
-    if (ubase) ubase[s.N] = u;
-    st->units = u;
+    share(W, &x0, &x1);
+    int run = 0;
+    for (int i0 = 0; i0 < items; i0 += nt) {
+      const int i = i0 + tid;
+      const int u = i < items ? units(i) : 0, c = i < items ? pd_chunks(pd_item_keys(s, i)) : 0;
+      int tot;
+      const int ex = run + block_exclusive_scan(u * c, scan_sh, &tot);
+      if (x0 >= ex && x0 < ex + u * c) place(i, u, c, x0 - ex, x1 - x0);
+      run += tot;
+    }
   }
-  __syncthreads();
-  const int x0 = st->x0;
-  run = 0;
-  for (int i0 = 0; i0 < items; i0 += nt) {
-    const int i = i0 + tid, w = weight(i);
-    int tot;
-    const int ex = run + block_exclusive_scan(w, scan_sh, &tot);
-    if (x0 >= ex && x0 < ex + w) {  // at most one item
-      st->item = i;
-      st->off = x0 - ex;
+  if (plan) {
+    if (tid == 0) {
+      plan->starts[items] = W;
       int u = 0;
-      for (int n = 0; n < min(i, s.N); ++n) u += pd_tiles(s, gs[n + 1] - gs[n]) * s.Hkv;
-      st->unit0 = u;
+      for (int n = 0; n < s.N; ++n) {
+        plan->ubase[n] = u;
+        u += units(n);
+      }
+      plan->ubase[s.N] = u;
     }
-    run += tot;
+    if (s.N > 0 && tid <= s.N) plan->gsan[tid] = gs[tid];
+    for (int b = tid; b < s.B; b += nt) {
+      int g = -1;
+      for (int n = 0; n < s.N; ++n)
+        if (gs[n] <= b && b < gs[n + 1]) g = n;
+      plan->group[b] = g;
+    }
   }
   __syncthreads();
 }
@@ -144,10 +179,10 @@ __device__ __forceinline__ void pd_locate(const PdShape& s, const int* gs, int c
 struct PdSeg {
   bool own;
   int n, b;        // prefix index, or sequence
-  int h, tile;
+  int h;
   int unit;        // index among the prefix units, or b * Hkv + h
   int rows;        // query rows of the tile
-  int row0;        // prefix: first row (sequence * G + head) of the tile
+  int row0;        // first row (sequence * G + head) of the tile
   int keys;        // keys of the unit
   int j0, j1;      // its chunks taken here
 };
@@ -156,61 +191,50 @@ struct PdSeg {
 struct PdWalk {
   const PdShape& s;
   const int* gs;
-  int left;        // chunks still to take
-  int item, off;   // current item, chunk offset in it
-  int unit0;
-  __device__ PdWalk(const PdShape& sh, const int* g, const PdStart& st)
-      : s(sh), gs(g), left(st.x1 - st.x0), item(st.item), off(st.off), unit0(st.unit0) {}
+  int left, item, h, tile, j, unit0;
+  int keys = 0, tiles = 0;  // of `item`, once loaded
+  bool loaded = false;
+  __device__ __forceinline__ PdWalk(const PdShape& sh, const int* g, const PdStart& st)
+      : s(sh), gs(g), left(st.left), item(st.item), h(st.h), tile(st.tile), j(st.j),
+        unit0(st.unit0) {}
   __device__ __forceinline__ bool next(PdSeg& q) {
-    while (left > 0) {
-      if (item < s.N) {
-        const int seqs = gs[item + 1] - gs[item], tiles = pd_tiles(s, seqs);
-        const int keys = pd_prefix_len(s, item), c = pd_chunks(keys);
-        const int ui = c > 0 ? off / c : 0;
-        if (ui >= tiles * s.Hkv || c == 0) {
+    if (left <= 0) return false;
+    while (!loaded) {
+      if (item >= s.N + s.B) return false;
+      keys = pd_item_keys(s, item);
+      tiles = item < s.N ? pd_tiles(s, gs[item + 1] - gs[item]) : 1;
+      loaded = keys > 0 && tiles > 0;
+      if (!loaded) {
+        unit0 += tiles * s.Hkv;  // only read for prefixes
+        ++item;
+      }
+    }
+    const int c = pd_chunks(keys);
+    q.own = item >= s.N;
+    q.n = q.own ? 0 : item;
+    q.b = q.own ? item - s.N : 0;
+    q.h = h;
+    q.keys = keys;
+    q.unit = q.own ? q.b * s.Hkv + h : unit0 + h * tiles + tile;
+    q.row0 = (q.own ? q.b : gs[item]) * s.G + tile * s.R;
+    q.rows = q.own ? s.G : min(s.R, (gs[item + 1] - gs[item]) * s.G - tile * s.R);
+    q.j0 = j;
+    q.j1 = min(c, j + left);
+    left -= q.j1 - j;
+    j = q.j1;
+    if (j == c) {
+      j = 0;
+      if (++tile == tiles) {
+        tile = 0;
+        if (++h == s.Hkv) {
+          h = 0;
           unit0 += tiles * s.Hkv;
           ++item;
-          off = 0;
-          continue;
+          loaded = false;
         }
-        q.own = false;
-        q.n = item;
-        q.b = 0;
-        q.h = ui / tiles;
-        q.tile = ui - q.h * tiles;
-        q.unit = unit0 + ui;
-        q.row0 = gs[item] * s.G + q.tile * s.R;
-        q.rows = min(s.R, seqs * s.G - q.tile * s.R);
-        q.keys = keys;
-        q.j0 = off - ui * c;
-        q.j1 = min(c, q.j0 + left);
-      } else {
-        const int b = item - s.N;
-        if (b >= s.B) return false;
-        const int keys = pd_own_len(s, b), c = pd_chunks(keys);
-        const int ui = c > 0 ? off / c : 0;
-        if (ui >= s.Hkv || c == 0) {
-          ++item;
-          off = 0;
-          continue;
-        }
-        q.own = true;
-        q.n = 0;
-        q.b = b;
-        q.h = ui;
-        q.tile = 0;
-        q.unit = b * s.Hkv + ui;
-        q.row0 = b * s.G;
-        q.rows = s.G;
-        q.keys = keys;
-        q.j0 = off - ui * c;
-        q.j1 = min(c, q.j0 + left);
       }
-      left -= q.j1 - q.j0;
-      off += q.j1 - q.j0;
-      return true;
     }
-    return false;
+    return true;
   }
 };
 
