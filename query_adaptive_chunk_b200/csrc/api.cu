@@ -1293,12 +1293,13 @@ csa_status prefix_sizes(csa_dtype dtype, int B, int Hq, int Hkv, int D, int N, i
   CSA_SUPPORT(N <= 64, "N must be <= 64");
   CSA_SUPPORT(static_cast<int64_t>(B) * Hkv <= 65535, "B*Hkv must be <= 65535");
   CSA_SUPPORT(Tp < 2147483584LL && T < 2147483584LL, "Tp and T must be < 2^31 - 64");
-  // the chunks of all units are numbered with 32 bits (row tiles of 32 at least)
-  const int64_t chunks = (static_cast<int64_t>(B) * (Hq / Hkv) / 32 + N) * Hkv * ((Tp + 63) / 64) +
-                         static_cast<int64_t>(B) * Hkv * ((T + 63) / 64);
-  CSA_SUPPORT(N == 0 ? static_cast<int64_t>(B) * Hkv * ((T + 63) / 64) < 2147483648LL
-                     : chunks < 2147483648LL,
-              "too many keys in all (chunks of 64 keys per row tile must be < 2^31)");
+  // the chunks of all units are numbered with 32 bits (16 keys and row tiles
+  // of 32 at least)
+  const int64_t U = static_cast<int64_t>(B) * Hkv;
+  const int64_t own = U * ((T + 15) / 16);
+  const int64_t pre = N == 0 ? 0 : (U * (Hq / Hkv) / 32 + static_cast<int64_t>(N) * Hkv) * ((Tp + 15) / 16);
+  CSA_SUPPORT(own < 2147483648LL && pre < 2147483648LL - own,
+              "too many keys in all (chunks of 16 keys, times row tiles, must be < 2^31)");
   return CSA_OK;
 }
 
@@ -1460,8 +1461,8 @@ int64_t csa_prefix_decode_workspace_bytes(csa_dtype dtype, int B, int Hq, int Hk
   if (prefix_sizes(dtype, B, Hq, Hkv, D, N, Tp, T) != CSA_OK) return -1;
   csa::Launch l;
   if (launch_ctx(nullptr, &l) != CSA_OK) return -1;
-  return csa::prefix_decode_workspace_bytes(dtype == CSA_BF16, B, Hkv, Hq / Hkv, D, N, T,
-                                            weights != 0, l.num_sms);
+  return csa::prefix_decode_workspace_bytes(dtype == CSA_BF16, B, Hkv, Hq / Hkv, D, N, Tp, T,
+                                            weights != 0 && T > 0, l.num_sms);
 }
 
 csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream) {
@@ -1497,8 +1498,8 @@ csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream)
   CSA_TRY(launch_ctx(stream, &l));
   const int G = d->Hq / d->Hkv;
   CSA_REQUIRE(d->workspace_bytes >= csa::prefix_decode_workspace_bytes(
-                                        d->dtype == CSA_BF16, d->B, d->Hkv, G, d->D, d->N, d->T,
-                                        d->weights != nullptr, l.num_sms),
+                                        d->dtype == CSA_BF16, d->B, d->Hkv, G, d->D, d->N, d->Tp, d->T,
+                                        d->weights != nullptr && d->T > 0, l.num_sms),
               "workspace smaller than csa_prefix_decode_workspace_bytes()");
   csa::PrefixDecodeArgs a{};
   a.bf16 = d->dtype == CSA_BF16;

@@ -1,12 +1,10 @@
 """Writes exp2_poly.h: coefficients of the cubic c0 + c1 f + c2 f^2 + c3 f^3
 that approximates 2^f on [-1/2, 1/2] with the smallest maximum RELATIVE
-error (minimax, found by the Remez exchange algorithm in float64), and
-exp2_poly5.h: the same of degree 5.
+error (minimax, found by the Remez exchange algorithm in float64).
 
-Used by the prefill kernel (degree 5: the shared-prefix decode, whose
-log-sum-exp and weights are fp32 results) to compute part of its exponentials
-on the FMA pipe (Cody-Waite style: 2^x = 2^j * 2^f with j = rint(x), f = x - j),
-so that the special-function unit is not the bottleneck.  Run:
+Used by the prefill kernel to compute part of its exponentials on the FMA
+pipe (Cody-Waite style: 2^x = 2^j * 2^f with j = rint(x), f = x - j), so
+that the special-function unit is not the bottleneck.  Run:
     python query_adaptive_chunk_b200/csrc/gen_exp2_poly.py
 """
 import os
@@ -51,21 +49,16 @@ def remez(deg=DEG, iters=30):
     return c, float(np.max(np.abs(err)))
 
 
-def write(name, deg, word, prefix):
-    c, e = remez(deg)
-    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), name)
+def main():
+    c, e = remez()
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "exp2_poly.h")
     with open(path, "w") as f:
-        f.write(f"// Generated by gen_exp2_poly.py: minimax (relative error) {word} for 2^f,\n")
+        f.write("// Generated by gen_exp2_poly.py: minimax (relative error) cubic for 2^f,\n")
         f.write(f"// f in [-1/2, 1/2], Remez exchange in float64; max relative error {e:.3e}.\n")
         f.write("#pragma once\n")
         for i, v in enumerate(c):
-            f.write(f"#define {prefix}{i} {np.float32(v)!r}f\n".replace("np.float32(", "").replace(")f", "f"))
+            f.write(f"#define CSA_EXP2_C{i} {np.float32(v)!r}f\n".replace("np.float32(", "").replace(")f", "f"))
     print(path, c, e)
-
-
-def main():
-    write("exp2_poly.h", DEG, "cubic", "CSA_EXP2_C")
-    write("exp2_poly5.h", 5, "quintic", "CSA_EXP2_Q")
 
 
 if __name__ == "__main__":

@@ -25,33 +25,35 @@ namespace {
 // of 64 keys held in shared memory.
 constexpr int kF32Rows = 32;
 constexpr int kF32Threads = 256;
+constexpr int kF32ChunkLog2 = 6, kF32Chunk = 1 << kF32ChunkLog2;
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 template <int D>
 __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams p) {
-  constexpr int KS = D + 4, SS = kPdChunk + 4;
+  constexpr int KS = D + 4, SS = kF32Chunk + 4;
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;                           // [32][KS]
   float* sk = sq + kF32Rows * KS;           // [64][KS]
-  float* sv = sk + kPdChunk * KS;           // [64][D]
-  float* ss = sv + kPdChunk * D;            // [32][SS]
+  float* sv = sk + kF32Chunk * KS;           // [64][D]
+  float* ss = sv + kF32Chunk * D;            // [32][SS]
   __shared__ int gs[kPdMaxPrefixes + 1];
   __shared__ PdStart st;
   __shared__ int scan_sh[33];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  if (tid < 32) pd_groups(p.s, gs);
-  const int key0 = tid < p.s.N + p.s.B ? pd_item_keys(p.s, tid) : 0;
+  const PdShape& shape = p.b.s;
+  if (tid < 32) pd_groups(shape, gs);
+  const int key0 = tid < shape.N + shape.B ? pd_item_keys(shape, tid) : 0;
   __syncthreads();
-  pd_locate(p.s, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.plan : nullptr);
-  PdWalk walk(p.s, gs, st);
+  pd_locate<1>(shape, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.b.plan : nullptr);
+  PdWalk walk(shape, gs, st);
   PdSeg g;
   while (walk.next(g)) {
     for (int i = tid; i < kF32Rows * (D / 4); i += kF32Threads) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < g.rows) {
-        const int row = g.row0 + r, b = row / p.s.G, hd = g.h * p.s.G + row % p.s.G;
+        const int row = g.row0 + r, b = row / shape.G, hd = g.h * shape.G + row % shape.G;
         x = ld4(static_cast<const float*>(p.q) + (static_cast<int64_t>(b) * p.Hq + hd) * D + d);
       }
       *reinterpret_cast<float4*>(sq + r * KS + d) = x;
@@ -68,9 +70,9 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) o[r][d] = 0.f;
     for (int j = g.j0; j < g.j1; ++j) {
-      const int t0 = j * kPdChunk, nk = min(kPdChunk, g.keys - t0);
+      const int t0 = j * kF32Chunk, nk = min(kF32Chunk, g.keys - t0);
       __syncthreads();  // the previous chunk's values have been read
-      for (int i = tid; i < kPdChunk * (D / 4); i += kF32Threads) {
+      for (int i = tid; i < kF32Chunk * (D / 4); i += kF32Threads) {
         const int t = i / (D / 4), d = (i % (D / 4)) * 4;
         // rows past the keys are zero: whatever the cache holds there, 0 * v stays 0
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
           mx = fmaxf(mx, s[r][c]);
         }
         if (g.own && p.logits && row < g.rows) {
-          float* lg = p.logits + (static_cast<int64_t>(g.unit) * p.s.G + row) * p.Tl + t0;
+          float* lg = p.logits + (static_cast<int64_t>(g.unit) * shape.G + row) * p.Tl + t0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) lg[tx + 16 * c] = s[r][c];
         }
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
       }
       __syncwarp();  // a row's weights are written and read by the same half-warp
 #pragma unroll 4
-      for (int t = 0; t < kPdChunk; ++t) {
+      for (int t = 0; t < kF32Chunk; ++t) {
         float pw[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) pw[r] = ss[(ty * 2 + r) * SS + t];
@@ -148,9 +150,9 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
       }
     }
     const int64_t slot = static_cast<int64_t>(blockIdx.x) + g.unit;
-    const int rows = g.own ? p.s.G : p.slot_rows;
-    float* po = (g.own ? p.oo : p.po) + slot * rows * D;
-    float* pl = (g.own ? p.olse : p.plse) + slot * rows;
+    const int rows = g.own ? shape.G : p.b.slot_rows;
+    float* po = (g.own ? p.oo : p.b.po) + slot * rows * D;
+    float* pl = (g.own ? p.olse : p.b.plse) + slot * rows;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = ty * 2 + r;
@@ -182,19 +184,17 @@ constexpr int kMaxG = 16;
 constexpr int kMergeSrcs = 64;       // partials per head whose factors are kept
 
 // Partials of one query head: `np` of its prefix unit, then `no` of its own
-// unit.  Partial i lies at row (i >> sh) * step + (i & sh) * half from the
-// unit's first: sh = 1 where a CTA's share is in two halves.
+// unit.  Prefix partial i lies at row (i >> psh) * pstep + (i & psh) * phalf
+// from the unit's first: psh = 1 where a CTA's share is in two halves.
 struct MergeSrc {
   const float *pl, *po, *ol, *oo;
   int np, no;
   int psh, pstep, phalf;
-  int osh, ostep, ohalf;
+  int ostep;
   __device__ __forceinline__ int64_t prow(int i) const {
     return static_cast<int64_t>(i >> psh) * pstep + (i & psh) * phalf;
   }
-  __device__ __forceinline__ int64_t orow(int i) const {
-    return static_cast<int64_t>(i >> osh) * ostep + (i & osh) * ohalf;
-  }
+  __device__ __forceinline__ int64_t orow(int i) const { return static_cast<int64_t>(i) * ostep; }
   __device__ __forceinline__ float lse(int i) const {
     return i < np ? pl[prow(i)] : ol[orow(i - np)];
   }
@@ -202,7 +202,7 @@ struct MergeSrc {
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, int share) {
-  const PdShape& s = p.s;
+  const PdShape& s = p.b.s;
   const int u = blockIdx.y, b = u / s.Hkv, h = u - b * s.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = pd_own_len(s, b);
@@ -215,42 +215,42 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's partials
   for (int g = warp; g < s.G; g += kMergeThreads / 32) {
     MergeSrc m{};
-    const int W = p.plan.starts[s.N + s.B], x_own = p.plan.starts[s.N + b];
-    const int n = s.N > 0 ? p.plan.group[b] : -1;
+    const int W = p.b.plan.starts[s.N + s.B], x_own = p.b.plan.starts[s.N + b];
+    const int n = s.N > 0 ? p.b.plan.group[b] : -1;
     if (n >= 0) {
-      const int g0 = p.plan.gsan[n], g1 = p.plan.gsan[n + 1];
-      const int x_pre = p.plan.starts[n], ub = p.plan.ubase[n];
-      const int c = pd_chunks(pd_prefix_len(s, n));
+      const int g0 = p.b.plan.gsan[n], seqs = p.b.plan.gsan[n + 1] - g0;
+      const PdLine& ln = p.a.s.P > 0 && seqs * s.G >= p.a.s.min_rows ? p.a : p.b;
+      const int x_pre = ln.plan.starts[n], ub = ln.plan.ubase[n];
+      const int Wl = ln.plan.starts[s.N + s.B];
+      const int c = pd_chunks(ln.s, pd_prefix_len(s, n));
       if (c > 0) {
-        const int seqs = g1 - g0, tiles = pd_tiles(s, seqs);
+        const int tiles = pd_tiles(ln.s, seqs), R = ln.s.R;
         int r = (b - g0) * s.G + g;
-        const int tile = r / s.R;
-        r -= tile * s.R;
-        const int rows = min(s.R, seqs * s.G - tile * s.R);
+        const int tile = r / R;
+        r -= tile * R;
+        const int rows = min(R, seqs * s.G - tile * R);
         const int ui = h * tiles + tile, x = x_pre + ui * c;
-        const int c0 = pd_cta_of(x, W, s.P), c1 = pd_cta_of(x + c - 1, W, s.P);
-        if (p.halves == 2) {
-          const int rh = s.R / 2;
+        const int c0 = pd_worker_of(x, Wl, ln.s.P), c1 = pd_worker_of(x + c - 1, Wl, ln.s.P);
+        if (ln.halves == 2) {
+          const int rh = R / 2;
           m.psh = rows <= rh ? 1 : 0;
-          if (r >= rh) r += p.slot_rows / 2 - rh;
+          if (r >= rh) r += ln.slot_rows / 2 - rh;
         }
-        const int64_t row = (static_cast<int64_t>(c0) + ub + ui) * p.slot_rows + r;
+        const int64_t row = (static_cast<int64_t>(c0) + ub + ui) * ln.slot_rows + r;
         m.np = (c1 - c0 + 1) << m.psh;
-        m.pl = p.plse + row;
-        m.po = p.po + row * D;
-        m.pstep = p.slot_rows;
-        m.phalf = p.slot_rows / 2;
+        m.pl = ln.plse + row;
+        m.po = ln.po + row * D;
+        m.pstep = ln.slot_rows;
+        m.phalf = ln.slot_rows / 2;
       }
     }
-    const int c = pd_chunks(len);
+    const int c = pd_chunks(s, len);
     if (c > 0) {
       const int x = x_own + h * c;
-      const int c0 = pd_cta_of(x, W, s.P), c1 = pd_cta_of(x + c - 1, W, s.P);
-      m.osh = p.halves - 1;
-      m.no = (c1 - c0 + 1) << m.osh;
-      m.ostep = p.halves * s.G;
-      m.ohalf = s.G;
-      const int64_t row = (static_cast<int64_t>(c0) + u) * m.ostep + g;
+      const int c0 = pd_worker_of(x, W, s.P), c1 = pd_worker_of(x + c - 1, W, s.P);
+      m.no = c1 - c0 + 1;
+      const int64_t row = (static_cast<int64_t>(c0) + u) * s.G + g;
+      m.ostep = s.G;
       m.ol = p.olse + row;
       m.oo = p.oo + row * D;
     }
@@ -371,63 +371,103 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, 
   }
 }
 
-struct PdLayout {
-  int64_t starts, ubase, gsan, group, plse, po, olse, oo, logits, total;
-  int64_t Tl, slots;
+int64_t round256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// Hands out the workspace's areas; with base = null only counts.
+struct Carver {
+  char* base;
+  int64_t at = 0;
+  template <typename T>
+  T* take(int64_t n) {
+    T* p = base ? reinterpret_cast<T*>(base + at) : nullptr;
+    at += round256(n * static_cast<int64_t>(sizeof(T)));
+    return p;
+  }
 };
 
-// CTAs that share the chunks: one per SM for bf16 (it takes the SM's whole
-// shared memory), two for fp32.
-int pd_parts(bool bf16, int num_sms) { return bf16 ? num_sms : 2 * num_sms; }
-int pd_rows(bool bf16, int G) { return bf16 ? pd_tc_rows(G) : kF32Rows; }
-int pd_slot_rows(bool bf16) { return bf16 ? kPdTcSlotRows : kF32Rows; }
-int pd_halves(bool bf16) { return bf16 ? 2 : 1; }
+void carve_line(Carver* c, PdLine* ln, int D, int64_t units) {
+  const PdShape& s = ln->s;
+  ln->plan.starts = c->take<int32_t>(s.N + s.B + 1);
+  ln->plan.ubase = c->take<int32_t>(s.N + 1);
+  ln->plan.gsan = c->take<int32_t>(s.N + 1);
+  ln->plan.group = c->take<int32_t>(s.B);
+  ln->slots = units > 0 ? s.P + units : 0;
+  ln->plse = c->take<float>(ln->slots * ln->slot_rows);
+  ln->po = c->take<float>(ln->slots * ln->slot_rows * D);
+}
 
-PdLayout pd_layout(bool bf16, int B, int Hkv, int G, int D, int N, int64_t T, bool weights, int P) {
-  const int64_t R = pd_rows(bf16, G), SR = pd_slot_rows(bf16), U = static_cast<int64_t>(B) * Hkv;
-  const int64_t pslots = N > 0 ? P + Hkv * (static_cast<int64_t>(B) * G / R + N) : 0;
-  const int64_t oslots = T > 0 ? P + U : 0;
-  PdLayout w{};
-  int64_t at = 0;
-  auto take = [&](int64_t bytes) {
-    const int64_t r = at;
-    at += (bytes + 255) / 256 * 256;
-    return r;
-  };
-  w.Tl = (T + kPdChunk - 1) / kPdChunk * kPdChunk;
-  w.starts = take(4ll * (N + B + 1));
-  w.ubase = take(4ll * (N + 1));
-  w.gsan = take(4ll * (N + 1));
-  w.group = take(4ll * B);
-  w.slots = pslots;
-  w.plse = take(4 * pslots * SR);
-  w.po = take(4 * pslots * SR * D);
-  w.olse = take(4 * oslots * pd_halves(bf16) * G);
-  w.oo = take(4 * oslots * pd_halves(bf16) * G * D);
-  w.logits = take(weights ? 4 * U * G * w.Tl : 0);
-  w.total = at;
-  return w;
+// The lines' shapes and the workspace (bytes returned).
+int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D, int N, int64_t Tp,
+                  int64_t T, bool weights, int num_sms) {
+  const int64_t rows = static_cast<int64_t>(B) * G, U = static_cast<int64_t>(B) * Hkv;
+  PdShape s{};
+  s.B = B;
+  s.Hkv = Hkv;
+  s.G = G;
+  s.N = N;
+  s.Tp = Tp;
+  s.T = T;
+  Carver c{ws};
+  p->a.s = p->b.s = s;
+  // fp32: one line of 32-row tiles, two CTAs per SM.  bf16: one CTA per SM for
+  // the groups of many rows, and the warps for everything else.
+  PdShape& a = p->a.s;
+  PdShape& b = p->b.s;
+  b.own = 1;
+  b.min_rows = 1;
+  if (bf16) {
+    a.R = pd_tc_rows(G);
+    a.P = N > 0 && Tp > 0 && rows > kPdFewRows ? num_sms : 0;
+    a.chunk_log2 = kPdTcChunkLog2;
+    a.min_rows = kPdFewRows + 1;
+    a.max_rows = 1 << 30;
+    p->a.halves = 2;
+    p->a.slot_rows = kPdTcSlotRows;
+    b.R = kPdFewRows;
+    b.P = kPdWarps * num_sms;
+    b.chunk_log2 = kPdWarpChunkLog2;
+    b.max_rows = kPdFewRows;
+    p->b.slot_rows = kPdFewRows;
+  } else {
+    b.R = kF32Rows;
+    b.P = 2 * num_sms;
+    b.chunk_log2 = kF32ChunkLog2;
+    b.max_rows = 1 << 30;
+    p->b.slot_rows = kF32Rows;
+  }
+  p->b.halves = 1;
+  // tiles of all groups: at most rows / R + N
+  if (a.P > 0) carve_line(&c, &p->a, D, Hkv * (rows / a.R + N));
+  carve_line(&c, &p->b, D, N > 0 && Tp > 0 ? Hkv * (bf16 ? N : rows / b.R + N) : 0);
+  const int64_t oslots = T > 0 ? b.P + U : 0;
+  p->olse = c.take<float>(oslots * G);
+  p->oo = c.take<float>(oslots * G * D);
+  p->Tl = (T + 63) / 64 * 64;
+  p->logits = c.take<float>(weights ? U * G * p->Tl : 0);
+  if (!weights) p->logits = nullptr;
+  return c.at;
 }
 
 template <int D>
 cudaError_t launch_attend_f32(const Launch& l, const PdParams& p) {
-  const int smem = ((kF32Rows + kPdChunk) * (D + 4) + kPdChunk * D + kF32Rows * (kPdChunk + 4)) * 4;
+  const int smem = ((kF32Rows + kF32Chunk) * (D + 4) + kF32Chunk * D + kF32Rows * (kF32Chunk + 4)) * 4;
   cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attend_f32_kernel<D><<<p.s.P, kF32Threads, smem, l.stream>>>(p);
+  attend_f32_kernel<D><<<p.b.s.P, kF32Threads, smem, l.stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_pd_merge(const Launch& l, const PdParams& p) {
   cudaLaunchConfig_t cfg = {};
-  const int64_t U = static_cast<int64_t>(p.s.B) * p.s.Hkv;
+  const PdShape& s = p.b.s;
+  const int64_t U = static_cast<int64_t>(s.B) * s.Hkv;
   int64_t blocks = 1;
   if (p.acc)  // about four CTAs per SM, of at least kMergeMinKeys keys
-    blocks = std::max<int64_t>(1, std::min<int64_t>((p.s.T + kMergeMinKeys - 1) / kMergeMinKeys,
+    blocks = std::max<int64_t>(1, std::min<int64_t>((s.T + kMergeMinKeys - 1) / kMergeMinKeys,
                                                     4ll * l.num_sms / U));
-  int64_t share = (p.s.T + blocks - 1) / blocks;
+  int64_t share = (s.T + blocks - 1) / blocks;
   share = std::max<int64_t>(4, (share + 3) / 4 * 4);
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(U));
   cfg.blockDim = dim3(kMergeThreads);
@@ -442,18 +482,23 @@ cudaError_t launch_pd_merge(const Launch& l, const PdParams& p) {
 
 }  // namespace
 
-int64_t prefix_decode_workspace_bytes(bool bf16, int B, int Hkv, int G, int D, int N, int64_t T,
-                                      bool weights, int num_sms) {
-  return pd_layout(bf16, B, Hkv, G, D, N, T, weights, pd_parts(bf16, num_sms)).total;
+int64_t prefix_decode_workspace_bytes(bool bf16, int B, int Hkv, int G, int D, int N, int64_t Tp,
+                                      int64_t T, bool weights, int num_sms) {
+  PdParams p{};
+  return pd_layout(&p, nullptr, bf16, B, Hkv, G, D, N, Tp, T, weights, num_sms);
 }
 
 cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std::string* why) {
-  const int G = a.Hq / a.Hkv, P = pd_parts(a.bf16, l.num_sms);
-  const PdLayout w = pd_layout(a.bf16, a.B, a.Hkv, G, a.D, a.N, a.T, a.weights != nullptr, P);
-  char* ws = static_cast<char*>(a.workspace);
   PdParams p{};
-  p.s = PdShape{a.B,  a.Hkv, G,            a.N,           pd_rows(a.bf16, G), P,
-                a.Tp, a.T,   a.prefix_len, a.group_start, a.len,           l.err};
+  const bool weights = a.weights != nullptr && a.T > 0;
+  pd_layout(&p, static_cast<char*>(a.workspace), a.bf16, a.B, a.Hkv, a.Hq / a.Hkv, a.D, a.N, a.Tp,
+            a.T, weights, l.num_sms);
+  for (PdShape* s : {&p.a.s, &p.b.s}) {
+    s->prefix_len = a.prefix_len;
+    s->group_start = a.group_start;
+    s->len = a.len;
+    s->err = l.err;
+  }
   p.q = a.q;
   p.Kp = a.Kp;
   p.Vp = a.Vp;
@@ -466,28 +511,19 @@ cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std
     p.vs[i] = a.vs[i];
   }
   p.Hq = a.Hq;
-  p.halves = pd_halves(a.bf16);
   p.scale_log2 = a.scale * kPdLog2e;
-  p.slot_rows = pd_slot_rows(a.bf16);
-  p.slots = w.slots;
-  p.plan = PdPlan{reinterpret_cast<int32_t*>(ws + w.starts), reinterpret_cast<int32_t*>(ws + w.ubase),
-                  reinterpret_cast<int32_t*>(ws + w.gsan), reinterpret_cast<int32_t*>(ws + w.group)};
-  p.plse = reinterpret_cast<float*>(ws + w.plse);
-  p.po = reinterpret_cast<float*>(ws + w.po);
-  p.olse = reinterpret_cast<float*>(ws + w.olse);
-  p.oo = reinterpret_cast<float*>(ws + w.oo);
-  p.logits = a.weights ? reinterpret_cast<float*>(ws + w.logits) : nullptr;
-  p.Tl = w.Tl;
   p.out = a.out;
   p.out_bf16 = a.out_bf16 ? 1 : 0;
   p.lse_out = a.lse_out;
-  p.acc = a.T > 0 ? a.weights : nullptr;
+  p.acc = weights ? a.weights : nullptr;
   p.decay = a.decay;
-  cudaError_t e;
-  if (a.bf16)
-    e = launch_attend_tc(l, p, a.D, why);
-  else
+  cudaError_t e = cudaSuccess;
+  if (a.bf16) {
+    if (p.a.s.P > 0) e = launch_attend_tc(l, p, a.D, why);
+    if (e == cudaSuccess) e = launch_attend_warp(l, p, a.D);
+  } else {
     e = a.D == 128 ? launch_attend_f32<128>(l, p) : launch_attend_f32<64>(l, p);
+  }
   if (e != cudaSuccess) return e;
   return a.D == 128 ? launch_pd_merge<128>(l, p) : launch_pd_merge<64>(l, p);
 }

@@ -8,22 +8,33 @@ namespace csa {
 constexpr float kPdLog2e = 1.4426950408889634f;
 constexpr float kPdLn2 = 0.6931471805599453f;
 
-struct PdParams {
+// bf16: groups of more rows than this go to the tensor-memory kernel
+// (prefix_decode_tc.cu), the others and the own units to the warps
+// (prefix_decode_warp.cu).
+constexpr int kPdFewRows = 16;
+
+// One kernel's line of units and where its partials go.  A prefix unit's slot
+// holds `slot_rows` rows, an own unit's G.  With halves = 2 row r of a tile
+// lies at (r / (R/2)) * slot_rows/2 + r % (R/2), and a unit of at most R / 2
+// rows is split once more inside its CTA: even chunks' rows in the slot's first
+// half, odd chunks' in its second.
+struct PdLine {
   PdShape s;
+  PdPlan plan;
+  int halves, slot_rows;
+  int64_t slots;  // prefix slots
+  float *plse, *po;
+};
+
+struct PdParams {
+  PdLine a;  // bf16: the groups of many rows; a.s.P = 0: no such line
+  PdLine b;  // the rest
   const void *q, *Kp, *Vp, *K, *V;
   int64_t kps[3], vps[3], ks[3], vs[3];  // strides in elements: prefix / sequence, head, token
   int Hq;
   float scale_log2;
-  // workspace.  A prefix unit's slot holds `slot_rows` rows, an own unit's
-  // `halves` * G.  With halves = 2 row r of a tile lies at (r / (R/2)) *
-  // slot_rows/2 + r % (R/2), and a unit of at most R / 2 rows (an own one always)
-  // is split once more inside its CTA: even chunks' rows in the slot's first
-  // half, odd chunks' in its second.
-  int halves, slot_rows;
-  int64_t slots;  // prefix slots
-  PdPlan plan;
-  float *plse, *po, *olse, *oo, *logits;
-  int64_t Tl;  // logits' row length
+  float *olse, *oo, *logits;  // own units' partials (line b) and logits
+  int64_t Tl;                 // logits' row length
   // outputs
   void* out;
   int out_bf16;
@@ -32,9 +43,15 @@ struct PdParams {
   float decay;
 };
 
-// prefix_decode_tc.cu: the bf16 attention kernel.
-int pd_tc_rows(int G);           // query rows per tile
+// prefix_decode_tc.cu: line a.
+int pd_tc_rows(int G);  // query rows per tile
 constexpr int kPdTcSlotRows = 256;
+constexpr int kPdTcChunkLog2 = 6;
 cudaError_t launch_attend_tc(const Launch& l, const PdParams& p, int D, std::string* why);
+
+// prefix_decode_warp.cu: line b of bf16.
+constexpr int kPdWarps = 8;
+constexpr int kPdWarpChunkLog2 = 4;
+cudaError_t launch_attend_warp(const Launch& l, const PdParams& p, int D);
 
 }  // namespace csa

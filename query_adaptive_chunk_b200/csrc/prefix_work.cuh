@@ -5,21 +5,21 @@
 //   prefix units (n, h, tile): the queries of up to R rows of the sequences of
 //     group n (row = sequence * G + head of the group) against prefix n;
 //   own units (b, h): the G query heads of one sequence against its own cache.
-// A unit's keys are cut into chunks of kPdChunk.  All chunks of all units lie
-// end to end (prefixes first; within a prefix by head, then row tile; own units by
-// sequence, then head) and CTA c of P = min(CTAs, W) takes chunks [W c / P,
-// W (c + 1) / P): every SM streams the same number of keys whatever the
-// lengths.  A CTA that holds any of unit i's chunks writes one partial
-// (normalised rows and their log2-sum-exp) to slot c + i: the pairs (c, i) met
-// along the line grow by one in c or in i at a time, so slots are distinct
-// and number at most P + units.
+// Units go to a kernel's line by their kind and by their group's rows.  A
+// unit's keys are cut into chunks.  All chunks of a line's units lie end to
+// end (prefixes first; within a prefix by head, then row tile; own units by
+// sequence, then head) and worker c (a CTA, or a warp) of P = min(workers, W)
+// takes chunks [W c / P, W (c + 1) / P): every SM streams the same number of
+// keys whatever the lengths.  A worker that holds any of unit i's chunks writes
+// one partial (normalised rows and their log2-sum-exp) to slot c + i: the
+// pairs (c, i) met along the line grow by one in c or in i at a time, so slots
+// are distinct and number at most P + units.
 #pragma once
 
 #include "internal.h"
 
 namespace csa {
 
-constexpr int kPdChunk = 64;      // keys per chunk
 constexpr int kPdMaxPrefixes = 64;
 
 // Sanitised lengths: out of range is flagged and clamped.
@@ -31,8 +31,14 @@ __device__ __forceinline__ int pd_clamp(int v, int64_t hi, const DevErr& e) {
   return v;
 }
 
+// A line of units.
 struct PdShape {
-  int B, Hkv, G, N, R, P;
+  int B, Hkv, G, N;
+  int R;                       // query rows per tile
+  int P;                       // workers
+  int chunk_log2;              // keys per chunk
+  int min_rows, max_rows;      // prefix units of groups of so many rows
+  int own;                     // own units too
   int64_t Tp, T;
   const int32_t* prefix_len;   // [N] or null: Tp
   const int32_t* group_start;  // [N + 1] or null: one group of all sequences
@@ -51,9 +57,13 @@ __device__ __forceinline__ int pd_own_len(const PdShape& s, int b) {
 __device__ __forceinline__ int pd_item_keys(const PdShape& s, int i) {
   return i < s.N ? pd_prefix_len(s, i) : pd_own_len(s, i - s.N);
 }
-__device__ __forceinline__ int pd_chunks(int keys) { return (keys + kPdChunk - 1) / kPdChunk; }
+__device__ __forceinline__ int pd_chunks(const PdShape& s, int keys) {
+  return (keys + (1 << s.chunk_log2) - 1) >> s.chunk_log2;
+}
+// Row tiles of a group of `seqs` sequences (0: the group is not on this line).
 __device__ __forceinline__ int pd_tiles(const PdShape& s, int seqs) {
-  return (seqs * s.G + s.R - 1) / s.R;
+  const int rows = seqs * s.G;
+  return rows < s.min_rows || rows > s.max_rows ? 0 : (rows + s.R - 1) / s.R;
 }
 
 // gs[0 .. N]: the groups' bounds, clamped to [0, B] and made non-decreasing
@@ -84,7 +94,7 @@ __device__ __forceinline__ void pd_groups(const PdShape& s, int* gs) {
   }
 }
 
-// A CTA's place on the line.
+// A worker's place on the line.
 struct PdStart {
   int left;             // its chunks
   int item, h, tile, j; // where they start: item, head, row tile, chunk of the unit
@@ -99,58 +109,62 @@ struct PdPlan {
   int32_t* group;   // [B] each sequence's prefix, or -1
 };
 
-// Block-wide: fills *st (shared).  `gs` (shared) is filled by pd_groups in the
-// calling code before a barrier; key0 = pd_item_keys of item threadIdx.x,
-// loaded before that barrier (any value for threads past the items).
+// Block-wide: fills st[0 .. NW - 1] (shared), the places of the block's NW
+// workers.  `gs` (shared) is filled by pd_groups in the calling code before a
+// barrier; key0 = pd_item_keys of item threadIdx.x, loaded before that barrier
+// (any value for threads past the items).
+template <int NW>
 __device__ __forceinline__ void pd_locate(const PdShape& s, const int* gs, int key0, PdStart* st,
                                           int* scan_sh, const PdPlan* plan) {
   const int items = s.N + s.B, nt = blockDim.x, tid = threadIdx.x;
   auto units = [&](int i) -> int {
-    return i < s.N ? pd_tiles(s, gs[i + 1] - gs[i]) * s.Hkv : s.Hkv;
+    return i < s.N ? pd_tiles(s, gs[i + 1] - gs[i]) * s.Hkv : s.own ? s.Hkv : 0;
   };
-  auto place = [&](int i, int u, int c, int off, int take) {  // one thread: CTA starts in item i
-    st->left = take;
-    st->item = i;
-    const int ui = off / c, tiles = i < s.N ? u / s.Hkv : 1;
-    st->h = ui / tiles;
-    st->tile = ui - st->h * tiles;
-    st->j = off - ui * c;
-    int before = 0;
-    for (int n = 0; n < min(i, s.N); ++n) before += units(n);
-    st->unit0 = before;
+  // chunks [ex, ex + u c) are item i's: the workers that start among them
+  auto place = [&](int W, int i, int u, int c, int ex) {
+    if (u * c == 0) return;
+    // at least one chunk for each worker that takes part: each writes the slots it owns
+    const int P = min(s.P, W), w0 = static_cast<int>(blockIdx.x) * NW;
+#pragma unroll 1
+    for (int k = 0; k < NW; ++k) {
+      if (w0 + k >= P) break;
+      const int x0 = static_cast<int>(static_cast<int64_t>(W) * (w0 + k) / P);
+      if (x0 < ex || x0 >= ex + u * c) continue;
+      const int off = x0 - ex, ui = off / c, tiles = i < s.N ? u / s.Hkv : 1;
+      int before = 0;
+      for (int n = 0; n < min(i, s.N); ++n) before += units(n);
+      st[k].left = static_cast<int>(static_cast<int64_t>(W) * (w0 + k + 1) / P) - x0;
+      st[k].item = i;
+      st[k].h = ui / tiles;
+      st[k].tile = ui - st[k].h * tiles;
+      st[k].j = off - ui * c;
+      st[k].unit0 = before;
+    }
   };
-  auto share = [&](int W, int* x0, int* x1) {
-    // at least one chunk for each CTA that takes part: each writes the slots it owns
-    const int P = max(1, min(s.P, W)), c = static_cast<int>(blockIdx.x);
-    *x0 = c < P ? static_cast<int>(static_cast<int64_t>(W) * c / P) : W;
-    *x1 = c < P ? static_cast<int>(static_cast<int64_t>(W) * (c + 1) / P) : W;
-  };
-  if (tid == 0) st->left = 0;
-  int W, x0, x1;
+  if (tid < NW) st[tid].left = 0;
+  int W;
   if (items <= nt) {
-    const int u = tid < items ? units(tid) : 0, c = tid < items ? pd_chunks(key0) : 0;
+    const int u = tid < items ? units(tid) : 0, c = tid < items ? pd_chunks(s, key0) : 0;
     const int ex = block_exclusive_scan(u * c, scan_sh, &W);
-    share(W, &x0, &x1);
-    if (x0 >= ex && x0 < ex + u * c) place(tid, u, c, x0 - ex, x1 - x0);  // at most one item
+    place(W, tid, u, c, ex);
     if (plan && tid < items) plan->starts[tid] = ex;
   } else {
     W = 0;
     for (int i0 = 0; i0 < items; i0 += nt) {
       const int i = i0 + tid;
       int tot;
-      const int ex = block_exclusive_scan(i < items ? units(i) * pd_chunks(pd_item_keys(s, i)) : 0,
-                                          scan_sh, &tot);
+      const int ex = block_exclusive_scan(
+          i < items ? units(i) * pd_chunks(s, pd_item_keys(s, i)) : 0, scan_sh, &tot);
       if (plan && i < items) plan->starts[i] = W + ex;
       W += tot;
     }
-    share(W, &x0, &x1);
     int run = 0;
     for (int i0 = 0; i0 < items; i0 += nt) {
       const int i = i0 + tid;
-      const int u = i < items ? units(i) : 0, c = i < items ? pd_chunks(pd_item_keys(s, i)) : 0;
+      const int u = i < items ? units(i) : 0, c = i < items ? pd_chunks(s, pd_item_keys(s, i)) : 0;
       int tot;
       const int ex = run + block_exclusive_scan(u * c, scan_sh, &tot);
-      if (x0 >= ex && x0 < ex + u * c) place(i, u, c, x0 - ex, x1 - x0);
+      place(W, i, u, c, ex);
       run += tot;
     }
   }
@@ -175,7 +189,7 @@ __device__ __forceinline__ void pd_locate(const PdShape& s, const int* gs, int k
   __syncthreads();
 }
 
-// One CTA's share of one unit.
+// One worker's share of one unit.
 struct PdSeg {
   bool own;
   int n, b;        // prefix index, or sequence
@@ -187,7 +201,7 @@ struct PdSeg {
   int j0, j1;      // its chunks taken here
 };
 
-// Walks a CTA's segments; every role of a CTA walks the same list.
+// Walks a worker's segments; every role of a CTA walks the same list.
 struct PdWalk {
   const PdShape& s;
   const int* gs;
@@ -202,14 +216,14 @@ struct PdWalk {
     while (!loaded) {
       if (item >= s.N + s.B) return false;
       keys = pd_item_keys(s, item);
-      tiles = item < s.N ? pd_tiles(s, gs[item + 1] - gs[item]) : 1;
+      tiles = item < s.N ? pd_tiles(s, gs[item + 1] - gs[item]) : s.own;
       loaded = keys > 0 && tiles > 0;
       if (!loaded) {
         unit0 += tiles * s.Hkv;  // only read for prefixes
         ++item;
       }
     }
-    const int c = pd_chunks(keys);
+    const int c = pd_chunks(s, keys);
     q.own = item >= s.N;
     q.n = q.own ? 0 : item;
     q.b = q.own ? item - s.N : 0;
@@ -238,9 +252,9 @@ struct PdWalk {
   }
 };
 
-// The CTA of `ctas` that holds chunk x of W.
-__device__ __forceinline__ int pd_cta_of(int x, int W, int ctas) {
-  const int P = min(ctas, W);
+// The worker of `workers` that holds chunk x of W.
+__device__ __forceinline__ int pd_worker_of(int x, int W, int workers) {
+  const int P = min(workers, W);
   return static_cast<int>(((static_cast<int64_t>(x) + 1) * P - 1) / W);
 }
 

@@ -8,7 +8,6 @@
 
 #include "common.cuh"
 #include "exp2_poly.h"
-#include "exp2_poly5.h"
 
 namespace csa {
 
@@ -146,24 +145,6 @@ __device__ __forceinline__ float2 exp2_fma2(float2 x) {
   float2 q = __ffma2_rn(f, make_float2(CSA_EXP2_C3, CSA_EXP2_C3), make_float2(CSA_EXP2_C2, CSA_EXP2_C2));
   q = __ffma2_rn(q, f, make_float2(CSA_EXP2_C1, CSA_EXP2_C1));
   q = __ffma2_rn(q, f, make_float2(CSA_EXP2_C0, CSA_EXP2_C0));
-  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
-}
-
-// The same with the quintic of exp2_poly5.h (relative error below 2e-7, as the
-// special-function unit's), for sums that become fp32 results.
-__device__ __forceinline__ float2 exp2_fma2_quintic(float2 x) {
-  x.x = fmaxf(x.x, -125.f);
-  x.y = fmaxf(x.y, -125.f);
-  const float2 magic = make_float2(12582912.f, 12582912.f);
-  const float2 t = __fadd2_rn(x, magic);
-  const float2 jf = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
-  const float2 f = __ffma2_rn(jf, make_float2(-1.f, -1.f), x);
-  float2 q = __ffma2_rn(f, make_float2(CSA_EXP2_Q5, CSA_EXP2_Q5), make_float2(CSA_EXP2_Q4, CSA_EXP2_Q4));
-  q = __ffma2_rn(q, f, make_float2(CSA_EXP2_Q3, CSA_EXP2_Q3));
-  q = __ffma2_rn(q, f, make_float2(CSA_EXP2_Q2, CSA_EXP2_Q2));
-  q = __ffma2_rn(q, f, make_float2(CSA_EXP2_Q1, CSA_EXP2_Q1));
-  q = __ffma2_rn(q, f, make_float2(CSA_EXP2_Q0, CSA_EXP2_Q0));
   return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
                      __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
 }
