@@ -39,13 +39,13 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
   float* ss = sv + kF32Chunk * D;            // [32][SS]
   __shared__ int gs[kPdMaxPrefixes + 1];
   __shared__ PdStart st;
-  __shared__ int scan_sh[33];
+  __shared__ uint64_t scan_sh[kF32Threads / 32];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const PdShape& shape = p.b.s;
   if (tid < 32) pd_groups(shape, gs);
-  const int key0 = tid < shape.N + shape.B ? pd_item_keys(shape, tid) : 0;
+  const int key0 = tid < shape.N + shape.B ? pd_raw_keys(shape, tid) : 0;
   __syncthreads();
-  pd_locate<1>(shape, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.b.plan : nullptr);
+  pd_locate<1>(shape, nullptr, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.b.plan : nullptr);
   PdWalk walk(shape, gs, st);
   PdSeg g;
   while (walk.next(g)) {
@@ -172,16 +172,16 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
 
 // ------------------------------------------------------------------ merge
 //
-// A CTA joins the partials of one (sequence, KV head) and adds the weights of
-// a share of its own keys; the first share's CTA writes the output.  Reads the
+// A CTA joins a share of the partials of one (sequence, KV head) into the
+// output and adds the weights of a share of its own keys.  Reads the
 // partials once (they sit in L2) and 4 bytes per head and own key.  Bound by
 // latency at the usual sizes, so each step's loads go out together: where the
-// partials lie, their lse, then their rows and the logits.  The shares are as
-// many as keep every SM busy with a few CTAs each.
+// partials lie, their lse, then their rows and the logits.  The shares (of the
+// output's columns and of the own keys) are as many as keep every SM busy with
+// a few CTAs each.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeMinKeys = 1024;  // own keys per share at least
 constexpr int kMaxG = 16;
-constexpr int kMergeSrcs = 64;       // partials per head whose factors are kept
 
 // Partials of one query head: `np` of its prefix unit, then `no` of its own
 // unit.  Prefix partial i lies at row (i >> psh) * pstep + (i & psh) * phalf
@@ -207,21 +207,26 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int len = pd_own_len(s, b);
   const int64_t k0 = static_cast<int64_t>(blockIdx.x) * share;
-  if (blockIdx.x > 0 && k0 >= len) return;
+  // this share's output: `tasks` groups of four columns from task0 on
+  constexpr int D4 = D / 4;
+  const int per = (s.G * D4 + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  const int task0 = static_cast<int>(blockIdx.x) * per;
+  const int tasks = min(per, s.G * D4 - task0);
+  if (tasks <= 0 && (p.acc == nullptr || k0 >= len)) return;
   __shared__ float lse2[kMaxG];
   __shared__ MergeSrc src[kMaxG];
-  __shared__ float fac[kMaxG][kMergeSrcs];
   __shared__ float4 red[kMergeThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's partials
   for (int g = warp; g < s.G; g += kMergeThreads / 32) {
     MergeSrc m{};
-    const int W = p.b.plan.starts[s.N + s.B], x_own = p.b.plan.starts[s.N + b];
+    const int W = p.b.plan.starts[s.N + s.B], P = p.b.plan.starts[s.N + s.B + 1];
+    const int x_own = p.b.plan.starts[s.N + b];
     const int n = s.N > 0 ? p.b.plan.group[b] : -1;
     if (n >= 0) {
       const int g0 = p.b.plan.gsan[n], seqs = p.b.plan.gsan[n + 1] - g0;
-      const PdLine& ln = p.a.s.P > 0 && seqs * s.G >= p.a.s.min_rows ? p.a : p.b;
+      const PdLine& ln = p.a.s.ctas > 0 && seqs * s.G >= p.a.s.min_rows ? p.a : p.b;
       const int x_pre = ln.plan.starts[n], ub = ln.plan.ubase[n];
-      const int Wl = ln.plan.starts[s.N + s.B];
+      const int Wl = ln.plan.starts[s.N + s.B], Pl = ln.plan.starts[s.N + s.B + 1];
       const int c = pd_chunks(ln.s, pd_prefix_len(s, n));
       if (c > 0) {
         const int tiles = pd_tiles(ln.s, seqs), R = ln.s.R;
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, 
         r -= tile * R;
         const int rows = min(R, seqs * s.G - tile * R);
         const int ui = h * tiles + tile, x = x_pre + ui * c;
-        const int c0 = pd_worker_of(x, Wl, ln.s.P), c1 = pd_worker_of(x + c - 1, Wl, ln.s.P);
+        const int c0 = pd_worker_of(x, Wl, Pl), c1 = pd_worker_of(x + c - 1, Wl, Pl);
         if (ln.halves == 2) {
           const int rh = R / 2;
           m.psh = rows <= rh ? 1 : 0;
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, 
     const int c = pd_chunks(s, len);
     if (c > 0) {
       const int x = x_own + h * c;
-      const int c0 = pd_worker_of(x, W, s.P), c1 = pd_worker_of(x + c - 1, W, s.P);
+      const int c0 = pd_worker_of(x, W, P), c1 = pd_worker_of(x + c - 1, W, P);
       m.no = c1 - c0 + 1;
       const int64_t row = (static_cast<int64_t>(c0) + u) * s.G + g;
       m.ostep = s.G;
@@ -255,79 +260,81 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, 
       m.oo = p.oo + row * D;
     }
     const int ns = m.np + m.no;
-    // the first two rounds (64 partials) stay in registers
-    float l0 = lane < ns ? m.lse(lane) : -INFINITY;
-    float l1 = lane + 32 < ns ? m.lse(lane + 32) : -INFINITY;
-    float mx = fmaxf(l0, l1);
-    for (int i = lane + 64; i < ns; i += 32) mx = fmaxf(mx, m.lse(i));
+    // the first 128 partials' stay in registers
+    float lv[4];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      lv[k] = lane + 32 * k < ns ? m.lse(lane + 32 * k) : -INFINITY;
+      mx = fmaxf(mx, lv[k]);
+    }
+    for (int i = lane + 128; i < ns; i += 32) mx = fmaxf(mx, m.lse(i));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float base = mx == -INFINITY ? 0.f : mx;
-    float sum = exp2f(l0 - base) + exp2f(l1 - base);
-    for (int i = lane + 64; i < ns; i += 32) sum += exp2f(m.lse(i) - base);
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum += exp2f(lv[k] - base);
+    for (int i = lane + 128; i < ns; i += 32) sum += exp2f(m.lse(i) - base);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float L = sum == 0.f ? -INFINITY : base + log2f(sum);
-    // a partial's share of the sum; 0 where its row was not written
-    fac[g][lane] = l0 == -INFINITY ? 0.f : exp2f(l0 - L);
-    fac[g][lane + 32] = l1 == -INFINITY ? 0.f : exp2f(l1 - L);
     if (lane == 0) {
       lse2[g] = L;
       src[g] = m;
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
-    constexpr int D4 = D / 4;
-    const int tasks = s.G * D4;
+  if (tasks > 0) {
+    // few tasks: several threads each, over the partials
     const int parts = max(1, kMergeThreads / tasks);
     for (int t0 = 0; t0 < tasks; t0 += kMergeThreads) {
       const int task = parts > 1 ? tid % tasks : t0 + tid, part = parts > 1 ? tid / tasks : 0;
-      const int g = task / D4, d = (task % D4) * 4;
+      const int g = (task0 + task) / D4, d = (task0 + task) % D4 * 4;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (task < tasks && part < parts) {
         const MergeSrc m = src[g];
         const float L = lse2[g];
         const int ns = L == -INFINITY ? 0 : m.np + m.no;
-        auto row = [&](int i) -> const float* {
-          return i < m.np ? m.po + m.prow(i) * D + d : m.oo + m.orow(i - m.np) * D + d;
-        };
-        auto add = [&](float w, const float4& v) {
-          o.x += w * v.x;
-          o.y += w * v.y;
-          o.z += w * v.z;
-          o.w += w * v.w;
-        };
-        const int nf = min(ns, kMergeSrcs);
-        for (int i = part; i < nf; i += 4 * parts) {  // four rows in flight
+        for (int i = part; i < ns; i += 4 * parts) {  // four rows in flight
           float w[4];
           float4 v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int j = i + k * parts;
-            w[k] = j < nf ? fac[g][j] : 0.f;
-            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (w[k] != 0.f) v[k] = ld4(row(j));  // (a NaN factor too)
+            const int j = min(i + k * parts, ns - 1);
+            w[k] = m.lse(j);
+            v[k] = ld4(j < m.np ? m.po + m.prow(j) * D + d : m.oo + m.orow(j - m.np) * D + d);
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) add(w[k], v[k]);
-        }
-        for (int i = kMergeSrcs + part; i < ns; i += parts) {
-          const float l = m.lse(i);
-          if (l != -INFINITY) add(exp2f(l - L), ld4(row(i)));
+          for (int k = 0; k < 4; ++k) {
+            // a row whose lse is -inf was not written
+            if (i + k * parts < ns && w[k] != -INFINITY) {
+              const float e = exp2f(w[k] - L);
+              o.x += e * v[k].x;
+              o.y += e * v[k].y;
+              o.z += e * v[k].z;
+              o.w += e * v[k].w;
+            }
+          }
         }
       }
       if (parts > 1) {
         red[tid] = o;
         __syncthreads();
-        if (part == 0) {
-          for (int k = 1; k < parts; ++k) {
-            const float4 v = red[tid + k * tasks];
+        // tree over the parts
+        int n = parts;
+        while (n > 1) {
+          const int half = (n + 1) / 2;
+          if (part < n - half && task < tasks) {
+            const float4 v = red[tid + half * tasks];
             o.x += v.x;
             o.y += v.y;
             o.z += v.z;
             o.w += v.w;
+            red[tid] = o;
           }
+          __syncthreads();
+          n = half;
         }
       }
       if (task < tasks && part == 0) {
@@ -342,9 +349,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, 
         }
       }
     }
-    if (p.lse_out && tid < s.G)
-      p.lse_out[static_cast<int64_t>(b) * p.Hq + h * s.G + tid] = lse2[tid] * kPdLn2;
   }
+  if (blockIdx.x == 0 && p.lse_out && tid < s.G)
+    p.lse_out[static_cast<int64_t>(b) * p.Hq + h * s.G + tid] = lse2[tid] * kPdLn2;
   if (p.acc != nullptr) {
     float* acc = p.acc + static_cast<int64_t>(u) * s.T;
     const float* lg = p.logits + static_cast<int64_t>(u) * s.G * p.Tl;
@@ -387,11 +394,11 @@ struct Carver {
 
 void carve_line(Carver* c, PdLine* ln, int D, int64_t units) {
   const PdShape& s = ln->s;
-  ln->plan.starts = c->take<int32_t>(s.N + s.B + 1);
+  ln->plan.starts = c->take<int32_t>(s.N + s.B + 2);
   ln->plan.ubase = c->take<int32_t>(s.N + 1);
   ln->plan.gsan = c->take<int32_t>(s.N + 1);
   ln->plan.group = c->take<int32_t>(s.B);
-  ln->slots = units > 0 ? s.P + units : 0;
+  ln->slots = units > 0 ? s.ctas * s.workers + units : 0;
   ln->plse = c->take<float>(ln->slots * ln->slot_rows);
   ln->po = c->take<float>(ln->slots * ln->slot_rows * D);
 }
@@ -417,29 +424,37 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
   b.min_rows = 1;
   if (bf16) {
     a.R = pd_tc_rows(G);
-    a.P = N > 0 && Tp > 0 && rows > kPdFewRows ? num_sms : 0;
+    a.ctas = N > 0 && Tp > 0 && rows > kPdFewRows ? num_sms : 0;
+    a.workers = 1;
+    a.first = 1;
+    // a chunk's time in 16-key steps of the warps: its bytes, and half as much
+    // again where both halves' rows are at work (groups taken as of equal size)
+    a.cost = 4.f * (N > 0 && rows / N > a.R / 2 ? 1.5f : 1.f);
+    b.cost = 1.f;
     a.chunk_log2 = kPdTcChunkLog2;
     a.min_rows = kPdFewRows + 1;
     a.max_rows = 1 << 30;
     p->a.halves = 2;
     p->a.slot_rows = kPdTcSlotRows;
     b.R = kPdFewRows;
-    b.P = kPdWarps * num_sms;
+    b.ctas = num_sms;
+    b.workers = kPdWarps;
     b.chunk_log2 = kPdWarpChunkLog2;
     b.max_rows = kPdFewRows;
     p->b.slot_rows = kPdFewRows;
   } else {
     b.R = kF32Rows;
-    b.P = 2 * num_sms;
+    b.ctas = 2 * num_sms;
+    b.workers = 1;
     b.chunk_log2 = kF32ChunkLog2;
     b.max_rows = 1 << 30;
     p->b.slot_rows = kF32Rows;
   }
   p->b.halves = 1;
   // tiles of all groups: at most rows / R + N
-  if (a.P > 0) carve_line(&c, &p->a, D, Hkv * (rows / a.R + N));
+  if (a.ctas > 0) carve_line(&c, &p->a, D, Hkv * (rows / a.R + N));
   carve_line(&c, &p->b, D, N > 0 && Tp > 0 ? Hkv * (bf16 ? N : rows / b.R + N) : 0);
-  const int64_t oslots = T > 0 ? b.P + U : 0;
+  const int64_t oslots = T > 0 ? b.ctas * b.workers + U : 0;
   p->olse = c.take<float>(oslots * G);
   p->oo = c.take<float>(oslots * G * D);
   p->Tl = (T + 63) / 64 * 64;
@@ -454,7 +469,7 @@ cudaError_t launch_attend_f32(const Launch& l, const PdParams& p) {
   cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attend_f32_kernel<D><<<p.b.s.P, kF32Threads, smem, l.stream>>>(p);
+  attend_f32_kernel<D><<<p.b.s.ctas, kF32Threads, smem, l.stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -463,10 +478,12 @@ cudaError_t launch_pd_merge(const Launch& l, const PdParams& p) {
   cudaLaunchConfig_t cfg = {};
   const PdShape& s = p.b.s;
   const int64_t U = static_cast<int64_t>(s.B) * s.Hkv;
-  int64_t blocks = 1;
-  if (p.acc)  // about four CTAs per SM, of at least kMergeMinKeys keys
-    blocks = std::max<int64_t>(1, std::min<int64_t>((s.T + kMergeMinKeys - 1) / kMergeMinKeys,
-                                                    4ll * l.num_sms / U));
+  // about four CTAs per SM: of at least kMergeMinKeys keys where there are
+  // weights, or of eight groups of columns where many partials may meet
+  const int64_t by_keys = p.acc ? (s.T + kMergeMinKeys - 1) / kMergeMinKeys : 1;
+  const int64_t by_cols = static_cast<int64_t>(s.G) * D / 32;
+  const int64_t blocks = std::max<int64_t>(
+      1, std::min<int64_t>(std::max(by_keys, by_cols), 4ll * l.num_sms / U));
   int64_t share = (s.T + blocks - 1) / blocks;
   share = std::max<int64_t>(4, (share + 3) / 4 * 4);
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(U));
@@ -519,7 +536,7 @@ cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std
   p.decay = a.decay;
   cudaError_t e = cudaSuccess;
   if (a.bf16) {
-    if (p.a.s.P > 0) e = launch_attend_tc(l, p, a.D, why);
+    if (p.a.s.ctas > 0) e = launch_attend_tc(l, p, a.D, why);
     if (e == cudaSuccess) e = launch_attend_warp(l, p, a.D);
   } else {
     e = a.D == 128 ? launch_attend_f32<128>(l, p) : launch_attend_f32<64>(l, p);

@@ -27,7 +27,7 @@ struct PdLine {
 };
 
 struct PdParams {
-  PdLine a;  // bf16: the groups of many rows; a.s.P = 0: no such line
+  PdLine a;  // bf16: the groups of many rows; a.s.ctas = 0: no such line
   PdLine b;  // the rest
   const void *q, *Kp, *Vp, *K, *V;
   int64_t kps[3], vps[3], ks[3], vs[3];  // strides in elements: prefix / sequence, head, token

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                              ~uintptr_t(1023));
   __shared__ int gs[kPdMaxPrefixes + 1];
   __shared__ PdStart st;
-  __shared__ int scan_sh[33];
+  __shared__ uint64_t scan_sh[kTcThreads / 32];
   const uint32_t sb = smem_u32(smem);
   const uint32_t sQ = sb + C::kQOff, sK = sb + C::kKOff, sV = sb + C::kVOff, bar = sb + C::kBarOff;
   const uint32_t q_full = bar, q_empty = bar + 16;  // [2 slots] each
@@ -171,14 +171,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   const PdShape& shape = p.a.s;
   const int items = shape.N + shape.B;
-  const int key0 = static_cast<int>(threadIdx.x) < items ? pd_item_keys(shape, threadIdx.x) : 0;
+  const int key0 = static_cast<int>(threadIdx.x) < items ? pd_raw_keys(shape, threadIdx.x) : 0;
   if (warp == 0) pd_groups(shape, gs);
+  if (threadIdx.x == 96) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
   if (warp == 1) tmem_alloc<512>(tmem_slot);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pd_locate<1>(shape, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.a.plan : nullptr);
+  pd_locate<1>(shape, &p.b.s, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.a.plan : nullptr);
   const int rh = shape.R / 2;
 
   PdWalk walk(shape, gs, st);
@@ -578,7 +583,7 @@ cudaError_t launch_tc(const Launch& l, const PdParams& p, std::string* why) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        TcCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  attend_tc_kernel<D><<<s.P, kTcThreads, TcCfg<D>::kSmem, l.stream>>>(k, v, q, qs, o, m, p);
+  attend_tc_kernel<D><<<s.ctas, kTcThreads, TcCfg<D>::kSmem, l.stream>>>(k, v, q, qs, o, m, p);
   return cudaGetLastError();
 }
 

@@ -58,13 +58,14 @@ __global__ void __launch_bounds__(kWThreads, 1) attend_warp_kernel(const PdParam
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int gs[kPdMaxPrefixes + 1];
   __shared__ PdStart st[kPdWarps];
-  __shared__ int scan_sh[33];
+  __shared__ uint64_t scan_sh[kPdWarps];
   const PdShape& shape = p.b.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int key0 = tid < shape.N + shape.B ? pd_item_keys(shape, tid) : 0;
+  const int key0 = tid < shape.N + shape.B ? pd_raw_keys(shape, tid) : 0;
   if (warp == 0) pd_groups(shape, gs);
   __syncthreads();
-  pd_locate<kPdWarps>(shape, gs, key0, st, scan_sh, blockIdx.x == 0 ? &p.b.plan : nullptr);
+  pd_locate<kPdWarps>(shape, p.a.s.ctas > 0 ? &p.a.s : nullptr, gs, key0, st, scan_sh,
+                      blockIdx.x == 0 ? &p.b.plan : nullptr);
 
   const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
   const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_normal();
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(kWThreads, 1) attend_warp_kernel(const PdParam
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+#pragma unroll 1
   for (int i = 0; i < C::kStages - 1; ++i) load_step(i);
 
   // ---- products
@@ -290,7 +292,7 @@ cudaError_t launch_w(const Launch& l, const PdParams& p) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.b.s.P / kPdWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.b.s.ctas));
   cfg.blockDim = dim3(kWThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = l.stream;
@@ -298,7 +300,7 @@ cudaError_t launch_w(const Launch& l, const PdParams& p) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.a.s.P > 0 ? 1 : 0;  // behind line a's kernel: fills the SMs it leaves
+  cfg.numAttrs = p.a.s.ctas > 0 ? 1 : 0;  // beside line a's kernel, on the SMs it leaves
   return cudaLaunchKernelEx(&cfg, attend_warp_kernel<D, NT>, p);
 }
 

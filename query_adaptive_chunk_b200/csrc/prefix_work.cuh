@@ -5,12 +5,14 @@
 //   prefix units (n, h, tile): the queries of up to R rows of the sequences of
 //     group n (row = sequence * G + head of the group) against prefix n;
 //   own units (b, h): the G query heads of one sequence against its own cache.
-// Units go to a kernel's line by their kind and by their group's rows.  A
-// unit's keys are cut into chunks.  All chunks of a line's units lie end to
-// end (prefixes first; within a prefix by head, then row tile; own units by
-// sequence, then head) and worker c (a CTA, or a warp) of P = min(workers, W)
-// takes chunks [W c / P, W (c + 1) / P): every SM streams the same number of
-// keys whatever the lengths.  A worker that holds any of unit i's chunks writes
+// Units go to one of two lines, each with a kernel, by their kind and by their
+// group's rows; the two kernels run side by side, each on the share of the
+// CTAs (one per SM) that its keys are of all, found on the device (one after
+// the other, the second's start-up would add to the first's).  A unit's keys
+// are cut into chunks.  All chunks of a line's units lie end to end (prefixes
+// first; within a prefix by head, then row tile; own units by sequence, then
+// head) and worker c (a CTA, or a warp) of P takes chunks [W c / P, W (c + 1) /
+// P): every SM streams the same number of keys whatever the lengths.  A worker that holds any of unit i's chunks writes
 // one partial (normalised rows and their log2-sum-exp) to slot c + i: the
 // pairs (c, i) met along the line grow by one in c or in i at a time, so slots
 // are distinct and number at most P + units.
@@ -35,10 +37,13 @@ __device__ __forceinline__ int pd_clamp(int v, int64_t hi, const DevErr& e) {
 struct PdShape {
   int B, Hkv, G, N;
   int R;                       // query rows per tile
-  int P;                       // workers
+  int ctas;                    // CTAs that both lines share (0: no such line)
+  int workers;                 // workers per CTA
   int chunk_log2;              // keys per chunk
   int min_rows, max_rows;      // prefix units of groups of so many rows
   int own;                     // own units too
+  int first;                   // the line launched first
+  float cost;                  // of a chunk, relative to the other line's
   int64_t Tp, T;
   const int32_t* prefix_len;   // [N] or null: Tp
   const int32_t* group_start;  // [N + 1] or null: one group of all sequences
@@ -53,7 +58,13 @@ __device__ __forceinline__ int pd_own_len(const PdShape& s, int b) {
   if (s.T == 0) return 0;
   return s.len ? pd_clamp(__ldg(s.len + b), s.T, s.err) : static_cast<int>(s.T);
 }
-// Keys of item i: prefix i, or the own cache of sequence i - N.
+// Item i: prefix i, or the own cache of sequence i - N.  Its keys as they
+// stand in memory (pd_raw_keys), and sanitised.
+__device__ __forceinline__ int pd_raw_keys(const PdShape& s, int i) {
+  if (i < s.N) return s.prefix_len ? __ldg(s.prefix_len + i) : static_cast<int>(s.Tp);
+  if (s.T == 0) return 0;
+  return s.len ? __ldg(s.len + i - s.N) : static_cast<int>(s.T);
+}
 __device__ __forceinline__ int pd_item_keys(const PdShape& s, int i) {
   return i < s.N ? pd_prefix_len(s, i) : pd_own_len(s, i - s.N);
 }
@@ -94,94 +105,153 @@ __device__ __forceinline__ void pd_groups(const PdShape& s, int* gs) {
   }
 }
 
-// A worker's place on the line.
+// A worker's place on the line: `left` chunks from chunk `off` of item `item`
+// on; unit0 prefix units lie before it (prefix items only).
 struct PdStart {
-  int left;             // its chunks
-  int item, h, tile, j; // where they start: item, head, row tile, chunk of the unit
-  int unit0;            // prefix units before `item` (prefix items only)
+  int left, item, off, unit0;
 };
 
 // What the merge needs to find a unit's partials, written by one CTA.
 struct PdPlan {
-  int32_t* starts;  // [N + B + 1] first chunk of each item, then W
+  int32_t* starts;  // [N + B + 2] first chunk of each item, then W, then P
   int32_t* ubase;   // [N + 1] first unit of each prefix
   int32_t* gsan;    // [N + 1] the sanitised group bounds
   int32_t* group;   // [B] each sequence's prefix, or -1
 };
 
+// Exclusive prefix sum over the block of two counts packed in 64 bits, one
+// barrier; `sh` holds one entry per warp.
+__device__ __forceinline__ uint64_t pd_scan(uint64_t v, uint64_t* sh, uint64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  uint64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  uint64_t w = lane < nw ? sh[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  *total = __shfl_sync(0xffffffffu, w, nw - 1);
+  const uint64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0) + x - v;
+}
+
+// Chunks of W before worker c of P (c <= P <= 2^15).
+__device__ __forceinline__ int pd_cut(int W, int c, int P) {
+  const int q = W / P;
+  return q * c + (W - q * P) * c / P;
+}
+
 // Block-wide: fills st[0 .. NW - 1] (shared), the places of the block's NW
-// workers.  `gs` (shared) is filled by pd_groups in the calling code before a
-// barrier; key0 = pd_item_keys of item threadIdx.x, loaded before that barrier
-// (any value for threads past the items).
+// workers on line `me`; `other` is the line beside it (null: none).  `gs`
+// (shared) is filled by pd_groups before a barrier; key0 = pd_raw_keys of item
+// threadIdx.x, loaded before that barrier (any value for threads past the
+// items).  At most 16 warps.
 template <int NW>
-__device__ __forceinline__ void pd_locate(const PdShape& s, const int* gs, int key0, PdStart* st,
-                                          int* scan_sh, const PdPlan* plan) {
-  const int items = s.N + s.B, nt = blockDim.x, tid = threadIdx.x;
-  auto units = [&](int i) -> int {
+__device__ __forceinline__ void pd_locate(const PdShape& me, const PdShape* other, const int* gs,
+                                          int key0, PdStart* st, uint64_t* scan_sh,
+                                          const PdPlan* plan) {
+  const int items = me.N + me.B, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31;
+  auto units = [&](const PdShape& s, int i) -> int {
     return i < s.N ? pd_tiles(s, gs[i + 1] - gs[i]) * s.Hkv : s.own ? s.Hkv : 0;
   };
-  // chunks [ex, ex + u c) are item i's: the workers that start among them
-  auto place = [&](int W, int i, int u, int c, int ex) {
-    if (u * c == 0) return;
-    // at least one chunk for each worker that takes part: each writes the slots it owns
-    const int P = min(s.P, W), w0 = static_cast<int>(blockIdx.x) * NW;
+  // chunks of item i on this line and, in the high half, the cost of both lines' shares
+  // of it: 16 keys' loads are 1, times 3/2 where both halves' rows are at work
+  auto weigh = [&](int i, int raw, int* mine) -> uint64_t {
+    *mine = 0;
+    if (i >= items) return 0;
+    const int keys = pd_clamp(raw, i < me.N ? me.Tp : me.T, me.err);
+    *mine = units(me, i) * pd_chunks(me, keys);
+    return static_cast<uint64_t>(static_cast<uint32_t>(*mine));
+  };
+  auto cost = [&](int i, int raw) -> uint64_t {  // of the other line's share, in its chunks
+    if (other == nullptr || i >= items) return 0;
+    const int keys = pd_clamp(raw, i < me.N ? me.Tp : me.T, me.err);
+    return static_cast<uint64_t>(units(*other, i) * pd_chunks(*other, keys)) << 32;
+  };
+  auto raw_of = [&](int i) { return i < items ? pd_raw_keys(me, i) : 0; };
+  if (tid < NW) st[tid].left = 0;
+  uint64_t total = 0, ex = 0;
+  int mine = 0;
+  const bool one = items <= nt;  // one item per thread
+  if (one) {
+    const uint64_t v = weigh(tid, key0, &mine) + cost(tid, key0);
+    ex = pd_scan(v, scan_sh, &total);
+  } else {
+    for (int i0 = 0; i0 < items; i0 += nt) {
+      const int i = i0 + tid, raw = raw_of(i);
+      const uint64_t v = weigh(i, raw, &mine) + cost(i, raw);
+      uint64_t tot;
+      pd_scan(v, scan_sh, &tot);
+      total += tot;
+      __syncthreads();  // scan_sh is used again
+    }
+  }
+  const int W = static_cast<int>(total & 0xffffffffu);
+  // this line's CTAs: its share of the keys, at least one for each line with work
+  int ctas = me.ctas;
+  const uint64_t wo = total >> 32;
+  if (wo > 0) {
+    const float cm = static_cast<float>(W) * me.cost, co = static_cast<float>(wo) * other->cost;
+    const int a = max(1, min(me.ctas - 1, __float2int_rn(me.ctas * (me.first ? cm : co) / (cm + co))));
+    ctas = W == 0 ? 1 : me.first ? a : me.ctas - a;
+  }
+  const int P = max(1, min(ctas * me.workers, W));  // each worker that takes part has a chunk
+  const int w0 = static_cast<int>(blockIdx.x) * NW;
+  const int c0 = min(P, w0 + min(lane, NW));  // lane k: where worker w0 + k starts
+  const int x_lane = pd_cut(W, c0, P);
+  auto place = [&](int i, int e, int n) {  // chunks [e, e + n) are item i's
 #pragma unroll 1
     for (int k = 0; k < NW; ++k) {
-      if (w0 + k >= P) break;
-      const int x0 = static_cast<int>(static_cast<int64_t>(W) * (w0 + k) / P);
-      if (x0 < ex || x0 >= ex + u * c) continue;
-      const int off = x0 - ex, ui = off / c, tiles = i < s.N ? u / s.Hkv : 1;
-      int before = 0;
-      for (int n = 0; n < min(i, s.N); ++n) before += units(n);
-      st[k].left = static_cast<int>(static_cast<int64_t>(W) * (w0 + k + 1) / P) - x0;
-      st[k].item = i;
-      st[k].h = ui / tiles;
-      st[k].tile = ui - st[k].h * tiles;
-      st[k].j = off - ui * c;
-      st[k].unit0 = before;
+      const int x0 = __shfl_sync(0xffffffffu, x_lane, k), x1 = __shfl_sync(0xffffffffu, x_lane, k + 1);
+      if (x1 > x0 && x0 >= e && x0 < e + n) {
+        st[k].left = x1 - x0;
+        st[k].item = i;
+        st[k].off = x0 - e;
+        int before = 0;
+        for (int m = 0; m < min(i, me.N); ++m) before += units(me, m);
+        st[k].unit0 = before;
+      }
     }
   };
-  if (tid < NW) st[tid].left = 0;
-  int W;
-  if (items <= nt) {
-    const int u = tid < items ? units(tid) : 0, c = tid < items ? pd_chunks(s, key0) : 0;
-    const int ex = block_exclusive_scan(u * c, scan_sh, &W);
-    place(W, tid, u, c, ex);
-    if (plan && tid < items) plan->starts[tid] = ex;
+  if (one) {
+    const int e = static_cast<int>(ex & 0xffffffffu);
+    place(tid, e, mine);
+    if (plan && tid < items) plan->starts[tid] = e;
   } else {
-    W = 0;
-    for (int i0 = 0; i0 < items; i0 += nt) {
-      const int i = i0 + tid;
-      int tot;
-      const int ex = block_exclusive_scan(
-          i < items ? units(i) * pd_chunks(s, pd_item_keys(s, i)) : 0, scan_sh, &tot);
-      if (plan && i < items) plan->starts[i] = W + ex;
-      W += tot;
-    }
     int run = 0;
     for (int i0 = 0; i0 < items; i0 += nt) {
       const int i = i0 + tid;
-      const int u = i < items ? units(i) : 0, c = i < items ? pd_chunks(s, pd_item_keys(s, i)) : 0;
-      int tot;
-      const int ex = run + block_exclusive_scan(u * c, scan_sh, &tot);
-      place(W, i, u, c, ex);
-      run += tot;
+      uint64_t tot;
+      const uint64_t v = weigh(i, raw_of(i), &mine);
+      const int e = run + static_cast<int>(pd_scan(v, scan_sh, &tot));
+      place(i, e, mine);
+      if (plan && i < items) plan->starts[i] = e;
+      run += static_cast<int>(tot);
+      __syncthreads();
     }
   }
   if (plan) {
     if (tid == 0) {
       plan->starts[items] = W;
+      plan->starts[items + 1] = P;
       int u = 0;
-      for (int n = 0; n < s.N; ++n) {
+      for (int n = 0; n < me.N; ++n) {
         plan->ubase[n] = u;
-        u += units(n);
+        u += units(me, n);
       }
-      plan->ubase[s.N] = u;
+      plan->ubase[me.N] = u;
     }
-    if (s.N > 0 && tid <= s.N) plan->gsan[tid] = gs[tid];
-    for (int b = tid; b < s.B; b += nt) {
+    if (me.N > 0 && tid <= me.N) plan->gsan[tid] = gs[tid];
+    for (int b = tid; b < me.B; b += nt) {
       int g = -1;
-      for (int n = 0; n < s.N; ++n)
+      for (int n = 0; n < me.N; ++n)
         if (gs[n] <= b && b < gs[n + 1]) g = n;
       plan->group[b] = g;
     }
@@ -205,12 +275,12 @@ struct PdSeg {
 struct PdWalk {
   const PdShape& s;
   const int* gs;
-  int left, item, h, tile, j, unit0;
+  int left, item, h = 0, tile = 0, j = 0, unit0;
+  int off;                  // chunks of `item` before the start
   int keys = 0, tiles = 0;  // of `item`, once loaded
   bool loaded = false;
   __device__ __forceinline__ PdWalk(const PdShape& sh, const int* g, const PdStart& st)
-      : s(sh), gs(g), left(st.left), item(st.item), h(st.h), tile(st.tile), j(st.j),
-        unit0(st.unit0) {}
+      : s(sh), gs(g), left(st.left), item(st.item), unit0(st.unit0), off(st.off) {}
   __device__ __forceinline__ bool next(PdSeg& q) {
     if (left <= 0) return false;
     while (!loaded) {
@@ -224,6 +294,13 @@ struct PdWalk {
       }
     }
     const int c = pd_chunks(s, keys);
+    if (off > 0) {  // the first segment of all
+      const int ui = off / c;
+      h = ui / tiles;
+      tile = ui - h * tiles;
+      j = off - ui * c;
+      off = 0;
+    }
     q.own = item >= s.N;
     q.n = q.own ? 0 : item;
     q.b = q.own ? item - s.N : 0;
@@ -252,10 +329,10 @@ struct PdWalk {
   }
 };
 
-// The worker of `workers` that holds chunk x of W.
-__device__ __forceinline__ int pd_worker_of(int x, int W, int workers) {
-  const int P = min(workers, W);
-  return static_cast<int>(((static_cast<int64_t>(x) + 1) * P - 1) / W);
+// The worker of P that holds chunk x of W: (x + 1) P - 1 < 2^46 is exact in
+// 64-bit floats, and the quotient is at least 2^-31 away from the next integer.
+__device__ __forceinline__ int pd_worker_of(int x, int W, int P) {
+  return static_cast<int>((static_cast<double>(x + 1) * P - 1.0) / W);
 }
 
 }  // namespace csa
