@@ -117,8 +117,8 @@ def _p(x):
 
 
 def _s(stream):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # torch.cuda.current_stream().cuda_stream, without its 3 us of wrapping
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -409,12 +409,6 @@ CSA_ROTARY_NONE, CSA_ROTARY_LINEAR, CSA_ROTARY_NTK, CSA_ROTARY_TURNS, CSA_ROTARY
 CSA_ROTARY_HALF, CSA_ROTARY_INTERLEAVED = 0, 1
 _ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "turns": 3, "ramp": 4}
 _ROTARY_LAYOUT = {"half": 0, "interleaved": 1}
-
-
-def _need(cond, why: str):
-    """The binding's own checks of tensor arguments, reported like the library's."""
-    if not cond:
-        raise CsaError(1, why)
 
 
 class RotaryDesc(ctypes.Structure):

@@ -291,24 +291,35 @@ class BlockSparsePrefill:
         return self.O
 
 
+def _bad(why: str):
+    raise csa.CsaError(1, why)
+
+
 def _same_device(device, **tensors):
     for name, t in tensors.items():
-        csa._need(t is None or t.device == device, f"{name} is on {None if t is None else t.device}, not {device}")
+        if t is not None and t.device != device:
+            _bad(f"{name} is on {t.device}, not {device}")
 
 
 def _rows(name, t, dtype, shape=None):
     """A tensor whose last index is dense: its other strides, in elements."""
-    csa._need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    csa._need(shape is None or tuple(t.shape) == tuple(shape),
-              f"{name} must have shape {shape}, not {None if shape is None else tuple(t.shape)}")
-    csa._need(t.stride(-1) == 1 or t.shape[-1] == 1, f"{name}: the last index must be dense")
-    return t.stride()[:-1]
+    if t.dtype != dtype:
+        _bad(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and t.shape != shape:
+        _bad(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] != 1:
+        _bad(f"{name}: the last index must be dense")
+    return st[:-1]
 
 
 def _dense(name, t, dtype, shape):
-    csa._need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    csa._need(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    csa._need(t.is_contiguous(), f"{name} must be contiguous")
+    if t.dtype != dtype:
+        _bad(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        _bad(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
     return t
 
 
@@ -328,6 +339,7 @@ class Rotary:
         self.table = torch.empty(rot // 2, dtype=torch.int64, device=device)
         if freqs is not None:
             freqs = _dense("freqs", freqs, torch.float64, (rot // 2,))
+        self.table_ptr = self.table.data_ptr()
         with torch.cuda.device(self.table.device):
             csa.csa_rotary_table(rot, theta, scaling, factor, orig_len, low, high, freqs,
                                  self.table)
@@ -342,28 +354,32 @@ class Rotary:
         transpose=True gives the gradient of the input from that of the output.
         Returns (q_out, k_out), or q_out alone without k."""
         B, S, Hq, D = q.shape
+        dt, dev = q.dtype, self.table.device
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        d = csa.RotaryDesc()
-        d.x, d.y, d.H = q.data_ptr(), q_out.data_ptr(), Hq
-        d.x_stride = csa._st3(*_rows("q", q, q.dtype))
-        d.y_stride = csa._st3(*_rows("q_out", q_out, q.dtype, q.shape))
+            q_out = torch.empty_like(q)
+        x = (q.data_ptr(), q_out.data_ptr(), Hq, _rows("q", q, dt),
+             _rows("q_out", q_out, dt, q.shape))
+        x2 = (None, None, 0, (0, 0, 0), (0, 0, 0))
         if k is not None:
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            d.x2, d.y2, d.H2 = k.data_ptr(), k_out.data_ptr(), k.shape[2]
-            d.x2_stride = csa._st3(*_rows("k", k, q.dtype, (B, S, k.shape[2], D)))
-            d.y2_stride = csa._st3(*_rows("k_out", k_out, q.dtype, k.shape))
-        _same_device(self.table.device, q=q, q_out=q_out, k=k, k_out=k_out, positions=positions)
+                k_out = torch.empty_like(k)
+            Hkv = k.shape[2]
+            x2 = (k.data_ptr(), k_out.data_ptr(), Hkv, _rows("k", k, dt, (B, S, Hkv, D)),
+                  _rows("k_out", k_out, dt, k.shape))
+            if k.device != dev or k_out.device != dev:
+                _bad(f"k and k_out must be on {dev}")
+        pos = stride = None
         if positions is not None:
-            csa._need(positions.dtype == torch.int32 and tuple(positions.shape) == (B, S),
-                      f"positions must be int32 of shape {(B, S)}")
-            csa._need(S == 1 or positions.stride(1) == 1, "positions: the token index must be dense")
-            d.positions, d.pos_stride_b = positions.data_ptr(), positions.stride(0)
-        d.dtype, d.B, d.S, d.D, d.rot = csa._dt(q.dtype), B, S, D, self.rot
-        d.layout, d.transpose, d.table = self.layout, int(transpose), self.table.data_ptr()
-        d.amplitude, d.pos0 = self.amplitude, pos0
-        csa.csa_rotary(d, stream=stream)
+            if positions.dtype != torch.int32 or positions.shape != (B, S) or positions.device != dev:
+                _bad(f"positions must be int32 of shape {(B, S)} on {dev}")
+            stride, s1 = positions.stride()
+            if S > 1 and s1 != 1:
+                _bad("positions: the token index must be dense")
+            pos = positions.data_ptr()
+        if q.device != dev or q_out.device != dev:
+            _bad(f"q and q_out must be on {dev}")
+        csa.csa_rotary(csa.RotaryDesc(*x, *x2, csa._dt(dt), B, S, D, self.rot, self.layout, transpose,
+                                      self.table_ptr, self.amplitude, pos, stride or 0, pos0), stream)
         return q_out if k is None else (q_out, k_out)
 
 
@@ -407,9 +423,9 @@ class TokenCache:
     def insert(self, k: torch.Tensor, v: torch.Tensor, stream=None):
         """One new token per active sequence, k and v [B, Hkv, D] (the last
         index dense): into the next free slot, or over the lightest unprotected."""
-        shape = (self.B, self.Hkv, self.D)
-        ks, vs = _rows("k", k, self.K.dtype, shape), _rows("v", v, self.K.dtype, shape)
-        csa.csa_cache_insert(self.desc, k, ks, v, vs, stream=stream)
+        shape, dt = (self.B, self.Hkv, self.D), self.K.dtype
+        csa.csa_cache_insert(self.desc, k, _rows("k", k, dt, shape), v, _rows("v", v, dt, shape),
+                             stream=stream)
 
     def compress(self, K: torch.Tensor, V: torch.Tensor, weights: torch.Tensor, *, lengths=None,
                  positions=None, next_pos=None, stream=None):
@@ -419,7 +435,8 @@ class TokenCache:
         the budget, in row order.  positions [B, Hkv, S] with next_pos [B], else
         the row numbers."""
         B, Hkv, S, D = K.shape
-        csa._need((B, Hkv, D) == (self.B, self.Hkv, self.D), "source K has other sizes than the cache")
+        if (B, Hkv, D) != (self.B, self.Hkv, self.D):
+            _bad("source K has other sizes than the cache")
         src = csa.cache_source(
             K=K, V=V, S=S, k_stride=_rows("source K", K, self.K.dtype),
             v_stride=_rows("source V", V, self.K.dtype, K.shape),
@@ -450,7 +467,8 @@ class SharedPrefixDecoder:
         kw = {}
         if Kp is not None:
             N, _, Tp, _ = Kp.shape
-            csa._need(Vp is not None, "Kp without Vp")
+            if Vp is None:
+                _bad("Kp without Vp")
             kw = dict(Kp=Kp, Vp=Vp, kp_stride=_rows("Kp", Kp, dt, (N, Hkv, Tp, D)),
                       vp_stride=_rows("Vp", Vp, dt, Kp.shape))
             if prefix_len is not None:
