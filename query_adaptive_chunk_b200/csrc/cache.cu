@@ -41,7 +41,7 @@ __device__ __forceinline__ void copy_row(void* dst, const void* src, int bytes, 
 //
 // Reads the unit's weights and positions once (8 bytes a slot), so it is
 // bound by latency at the usual sizes: one CTA per unit, the minimum of
-// (key << 32 | slot) over its threads, four slots in flight per thread, then
+// (key << 32 | slot) over its threads, eight slots in flight per thread, then
 // the first warps write the new row.  The sequence's length and next position are shared
 // by its heads: each CTA reads them before it arrives at the sequence's
 // counter, and the last one to arrive advances them and clears the counter.
@@ -52,34 +52,44 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
     int64_t kh, int64_t vb, int64_t vh, int wide, DevErr err) {
   __shared__ int sh_len, sh_next;
   __shared__ unsigned long long sh_best[kInsThreads / 32];
+  constexpr int U = 8;  // slots in flight per thread
   const int u = blockIdx.x, b = u / c.Hkv, h = u - b * c.Hkv, tid = threadIdx.x;
+  const float* w = c.weights + static_cast<int64_t>(u) * c.T;
+  const int32_t* pos = c.positions + static_cast<int64_t>(u) * c.T;
+  float x[U];
+  int p[U];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = j0 + i * kInsThreads;
+      x[i] = j < c.budget ? w[j] : 0.f;
+      p[i] = j < c.budget ? pos[j] : 0;
+    }
+  };
+  int arrived = -1;
   if (tid == 0) {
-    sh_len = *static_cast<volatile int32_t*>(c.len + b);
-    sh_next = *static_cast<volatile int32_t*>(c.next_pos + b);
+    const int n = *static_cast<volatile int32_t*>(c.len + b);
+    const int at = *static_cast<volatile int32_t*>(c.next_pos + b);
+    sh_len = n;
+    sh_next = at;
+    __threadfence();
+    if (at >= 0 && n >= 0 && n <= c.budget) arrived = atomicAdd(c.counters + b, 1);
   }
+  load(tid);  // most often the cache is full: its slots' loads go out beside the length's
   __syncthreads();
   const int len = sh_len, next = sh_next;
-  if (next < 0) return;  // an inactive sequence: nothing is read or written
+  if (next < 0) return;  // an inactive sequence: left alone
   if (len < 0 || len > c.budget) {
     if (tid == 0) dev_flag(err, DEV_BAD_INDEX);
     return;
   }
   int slot = len;
   if (len == c.budget) {
-    const float* w = c.weights + static_cast<int64_t>(u) * c.T;
-    const int32_t* pos = c.positions + static_cast<int64_t>(u) * c.T;
     unsigned long long best = ~0ull;
-    for (int j0 = tid; j0 < len; j0 += 4 * kInsThreads) {
-      float x[4];
-      int p[4];
+    for (int j0 = tid; j0 < len; j0 += U * kInsThreads) {
+      if (j0 != tid) load(j0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = j0 + i * kInsThreads;
-        x[i] = j < len ? w[j] : 0.f;
-        p[i] = j < len ? pos[j] : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < U; ++i) {
         const int j = j0 + i * kInsThreads;
         if (j < len && !is_protected(p[i], next, c.n_sink, c.n_local)) {
           const unsigned long long e =
@@ -118,14 +128,11 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
   } else if (tid == 0) {
     dev_flag(err, DEV_BAD_INDEX);  // every slot protected: positions are not distinct
   }
-  if (tid == 0) {
+  if (arrived == c.Hkv - 1) {  // thread 0 of the sequence's last head to have read these
     __threadfence();
-    if (atomicAdd(c.counters + b, 1) == c.Hkv - 1) {
-      __threadfence();
-      c.counters[b] = 0;
-      c.len[b] = len < c.budget ? len + 1 : len;
-      c.next_pos[b] = next + 1;
-    }
+    c.counters[b] = 0;
+    c.len[b] = len < c.budget ? len + 1 : len;
+    c.next_pos[b] = next + 1;
   }
 }
 
@@ -137,8 +144,13 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
 // budget-th largest key tau, the CTAs' histograms of each pass added through
 // distributed shared memory; keys equal to tau are taken lowest row first.
 // Each CTA writes its kept rows, ascending, into the destination's positions
-// (as row numbers; the copy turns them into positions).  The weights are
-// read once; bound by the passes' latency (4 cluster round trips).
+// (as row numbers; the copy turns them into positions).  Each warp takes a run of
+// consecutive keys, a lane per key, so that counts and places come from
+// ballots and shared memory is read without bank conflicts (the histograms by
+// atomics on one copy per warp; a match of equal buckets first took four
+// times as long).  The weights are
+// read once, eight a thread in flight; bound by the passes' latency (4 with two
+// cluster barriers each).
 constexpr int kCmpThreads = 512;
 constexpr int kCmpKeys = 49152;  // keys held per CTA (192 KB)
 
@@ -170,6 +182,7 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
   if (CS > 1) cluster_arrive_relaxed();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ unsigned int hw[kCmpThreads / 32][256];  // a histogram per warp: no contention between them
   __shared__ unsigned int hc[256], gc[256];
   __shared__ unsigned int part_eq[CS], part_sel[CS];
   __shared__ int scan_sh[33];
@@ -194,27 +207,51 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
     return;
   }
   const bool held = p.held != 0;
-  if (held)
-    for (int j = tid; j < n; j += kCmpThreads) keys[j] = make_key(j);
+  if (held) {
+    constexpr int U = 8;  // loads in flight
+    for (int j0 = tid; j0 < n; j0 += U * kCmpThreads) {
+      float w[U];
+      int pos[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int j = j0 + i * kCmpThreads;
+        w[i] = j < n ? wrow[j] : 0.f;
+        pos[i] = prow && j < n ? prow[j] : lo + j;
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int j = j0 + i * kCmpThreads;
+        if (j < n)
+          keys[j] = is_protected(pos[i], next, p.n_sink, p.n_local) ? kKeyProtected : weight_key(w[i]);
+      }
+    }
+  }
   auto key_at = [&](int j) -> uint32_t { return held ? keys[j] : make_key(j); };
+  __syncthreads();
+  // this warp's run of the CTA's rows
+  constexpr int kWarps = kCmpThreads / 32;
+  const int warp = tid >> 5;
+  const int run = (n + kWarps * 32 - 1) / (kWarps * 32) * 32;
+  const int s0 = min(n, warp * run), s1 = min(n, s0 + run);
   // keys > tau are taken, and the first `need` keys equal to tau
   uint32_t prefix = 0u, mask = 0u;
   unsigned int need = static_cast<unsigned int>(p.budget);
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int d = tid; d < 256; d += kCmpThreads) hc[d] = 0u;
-    __syncthreads();
-    for (int j0 = 0; j0 < n; j0 += kCmpThreads) {
-      const int j = j0 + tid;
-      int d = -1;
-      if (j < n) {
+    for (int d = lane; d < 256; d += 32) hw[warp][d] = 0u;
+    __syncwarp();
+    for (int j0 = s0; j0 < s1; j0 += 32) {
+      const int j = j0 + lane;
+      if (j < s1) {
         const uint32_t key = key_at(j);
-        if ((key & mask) == prefix) d = static_cast<int>((key >> shift) & 255u);
+        if ((key & mask) == prefix) atomicAdd(&hw[warp][(key >> shift) & 255u], 1u);
       }
-      const unsigned int act = __ballot_sync(0xffffffffu, d >= 0);
-      if (d >= 0) {  // one shared atomic per distinct bucket of the warp
-        const unsigned int peers = __match_any_sync(act, d);
-        if (lane == __ffs(peers) - 1) atomicAdd(&hc[d], static_cast<unsigned int>(__popc(peers)));
-      }
+    }
+    __syncthreads();
+    if (tid < 256) {
+      unsigned int sum = 0u;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += hw[w][tid];
+      hc[tid] = sum;
     }
     if (CS > 1) {
       cluster_arrive();  // every CTA's histogram of this pass is complete
@@ -275,16 +312,18 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
     __syncthreads();  // pick_sh read before the next pass writes it
   }
   const uint32_t tau = prefix;
-  const int seg = (n + kCmpThreads - 1) / kCmpThreads;
-  const int s0 = min(n, tid * seg), s1 = min(n, s0 + seg);
+  // of this warp's run: keys above tau, keys at tau
   int c_gt = 0, c_eq = 0;
-  for (int j = s0; j < s1; ++j) {
-    const uint32_t key = key_at(j);
-    c_gt += key > tau;
-    c_eq += key == tau;
+  for (int j0 = s0; j0 < s1; j0 += 32) {
+    const bool in = j0 + lane < s1;
+    const uint32_t key = in ? key_at(j0 + lane) : 0u;
+    c_gt += __popc(__ballot_sync(0xffffffffu, in && key > tau));
+    c_eq += __popc(__ballot_sync(0xffffffffu, in && key == tau));
   }
+  // lane 0 speaks for its warp in the block's sums
   int eq_tot = 0, eq_before = 0;
-  const int eq_base = block_exclusive_scan(c_eq, scan_sh, &eq_tot);
+  const int eq_base = __shfl_sync(
+      0xffffffffu, block_exclusive_scan(lane == 0 ? c_eq : 0, scan_sh, &eq_tot), 0);
   if (CS > 1) {
     if (tid < CS)
       st_cluster_u32(cluster_map(smem_u32(part_eq + rank), tid), static_cast<unsigned int>(eq_tot));
@@ -295,7 +334,8 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
   const int take = max(0, min(static_cast<int>(need) - eq_before, eq_tot));  // ties kept here
   const int c_sel = c_gt + max(0, min(take - eq_base, c_eq));
   int sel_tot = 0, sel_before = 0;
-  const int sel_base = block_exclusive_scan(c_sel, scan_sh, &sel_tot);
+  const int sel_base = __shfl_sync(
+      0xffffffffu, block_exclusive_scan(lane == 0 ? c_sel : 0, scan_sh, &sel_tot), 0);
   if (CS > 1) {
     if (tid < CS)
       st_cluster_u32(cluster_map(smem_u32(part_sel + rank), tid),
@@ -305,17 +345,17 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
     for (int r = 0; r < rank; ++r) sel_before += static_cast<int>(part_sel[r]);
   }
   int at = sel_before + sel_base, eq_seen = eq_base;
-  for (int j = s0; j < s1; ++j) {
-    const uint32_t key = key_at(j);
-    bool t = key > tau;
-    if (key == tau) {
-      t = eq_seen < take;
-      ++eq_seen;
-    }
-    if (t) {
-      if (at < p.budget) out[at] = lo + j;
-      ++at;
-    }
+  const unsigned int below = (1u << lane) - 1u;
+  for (int j0 = s0; j0 < s1; j0 += 32) {
+    const bool in = j0 + lane < s1;
+    const uint32_t key = in ? key_at(j0 + lane) : 0u;
+    const unsigned int eq = __ballot_sync(0xffffffffu, in && key == tau);
+    const bool t = in && (key > tau || (key == tau && eq_seen + __popc(eq & below) < take));
+    const unsigned int sel = __ballot_sync(0xffffffffu, t);
+    const int to = at + __popc(sel & below);
+    if (t && to < p.budget) out[to] = lo + j0 + lane;
+    at += __popc(sel);
+    eq_seen += __popc(eq);
   }
 }
 
@@ -394,11 +434,9 @@ __global__ void __launch_bounds__(kCopyThreads) compress_copy_kernel(const CopyP
 template <int CS>
 cudaError_t launch_compress_select(const Launch& l, const CompressParams& p, int U, size_t smem) {
   const void* fn = reinterpret_cast<const void*>(compress_select_kernel<CS>);
-  if (smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(U) * CS);
   cfg.blockDim = dim3(kCmpThreads);
@@ -440,9 +478,9 @@ cudaError_t launch_cache_compress(const Launch& l, const CacheArgs& dst, const C
     CompressParams p{s.weights, s.positions,  s.len,       s.next_pos, s.S,           dst.Hkv,
                      dst.budget, dst.n_sink, dst.n_local, dst.T,      dst.positions, 0,
                      l.err};
-    // CTAs per unit: about 4096 rows each, while the units alone leave SMs idle
+    // CTAs per unit: 2048 rows or more each, while all run at once (two per SM)
     int CS = 1;
-    while (CS < 8 && s.S > 4096ll * CS && 2ll * U * CS <= 2ll * l.num_sms) CS *= 2;
+    while (CS < 8 && s.S > 2048ll * CS && U * CS <= l.num_sms) CS *= 2;
     while (CS < 8 && (s.S + CS - 1) / CS > kCmpKeys) CS *= 2;
     const int64_t per = (s.S + CS - 1) / CS;
     p.held = per <= kCmpKeys ? 1 : 0;
