@@ -133,7 +133,7 @@ __device__ __forceinline__ uint64_t pd_scan(uint64_t v, uint64_t* sh, uint64_t* 
   __syncthreads();
   uint64_t w = lane < nw ? sh[lane] : 0;
 #pragma unroll
-  for (int o = 1; o < 16; o <<= 1) {
+  for (int o = 1; o < 32; o <<= 1) {
     const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += y;
   }
@@ -152,7 +152,7 @@ __device__ __forceinline__ int pd_cut(int W, int c, int P) {
 // workers on line `me`; `other` is the line beside it (null: none).  `gs`
 // (shared) is filled by pd_groups before a barrier; key0 = pd_raw_keys of item
 // threadIdx.x, loaded before that barrier (any value for threads past the
-// items).  At most 16 warps.
+// items).
 template <int NW>
 __device__ __forceinline__ void pd_locate(const PdShape& me, const PdShape* other, const int* gs,
                                           int key0, PdStart* st, uint64_t* scan_sh,
