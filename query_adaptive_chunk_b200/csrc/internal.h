@@ -227,9 +227,9 @@ bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t cols, uint64
                        uint64_t n1, uint64_t n2, uint64_t row_stride, uint64_t s1, uint64_t s2,
                        uint32_t box_rows, uint32_t box_cols, std::string* why);
 
-// bf16 or fp32 [n1, rows, cols] (n1 = 0: two-dimensional), 128-byte swizzle or none.
+// bf16 or fp32 [n1, rows, cols] (n1 = 0: two-dimensional), 128- or 64-byte swizzle.
 bool make_tmap_3d(CUtensorMap* map, const void* base, bool f32, uint64_t cols, uint64_t rows,
                   uint64_t n1, uint64_t row_stride, uint64_t s1, uint32_t box_cols,
-                  uint32_t box_rows, uint32_t box_n1, bool swizzle, std::string* why);
+                  uint32_t box_rows, uint32_t box_n1, int swizzle, std::string* why);
 
 }  // namespace csa

@@ -21,13 +21,13 @@
 // Bound: a CTA's chunk is 256 D bytes of K and V.  At the copy rate an SM gets about
 // 23 bytes a clock, 1430 clocks a chunk at D = 128, against 640 clocks of
 // products (QK^T at N = 64 is bound by its shared-memory operands) and 512 of
-// exponentials per half: up to 128 rows memory is the bound (prefix of 128K
-// tokens, 8 KV heads: 85% of the copy rate); with 256 rows the two warps per
-// scheduler take 2100 clocks a chunk, in which neither the special-function
-// unit (44%) nor the tensor cores (42%) are full.  Measured and not kept there:
-// half or a quarter of the exponentials on the FMA pipe (8% and 6% slower: the
-// issue slots are dearer than the unit), turns between the halves at the
-// exponentials (4% slower: the hand-over costs what the unit's sharing did).
+// exponentials per half: up to 128 rows memory is the bound (128K tokens, 8 KV
+// heads, 128 rows: 95 us, 87% of the copy rate).  With 256 rows a chunk takes
+// about 2000 clocks (151 us): the tensor pipe passes between the four groups of
+// products per chunk (QK^T and PV of each half), each short.  Measured there
+// and not kept: half or a quarter of the exponentials on the FMA pipe (8% and 6%
+// slower), four softmax warps per scheduler instead of two, a column half each
+// (9%), P written over S with QK^T two chunks ahead (9%).
 // The keys past a unit's end are masked in S, and their V rows zeroed in
 // shared memory, so that neither value reaches a result (0 * NaN is NaN).
 //
@@ -43,7 +43,7 @@
 namespace csa {
 namespace {
 
-constexpr int kTcThreads = 640;
+constexpr int kTcThreads = 384;
 constexpr float kTcRescaleLog2 = 8.0f;
 constexpr int kChunk = 1 << kPdTcChunkLog2;
 
@@ -54,13 +54,12 @@ struct TcCfg {
   // K and V have rings of their own: a K chunk is free after its QK^T, a V
   // chunk only after the softmax and PV behind it, and each half looks one
   // QK^T ahead (with one ring of 4 stages all were held and none loading)
-  static constexpr int kNK = 4 * 128 / D, kNV = 4 * 128 / D;
+  static constexpr int kNK = 4 * 128 / D, kNV = 5 * 128 / D;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = 2 * kQSlot;
   static constexpr int kVOff = kKOff + kNK * kKV;
-  static constexpr int kOOff = kVOff + kNV * kKV;  // 1 KB of output rows per softmax warp
-  static constexpr int kXOff = kOOff + 16 * 1024;  // [2][2 halves][2 column groups][128] floats
-  static constexpr int kBarOff = kXOff + 4096;
+  static constexpr int kOOff = kVOff + kNV * kKV;  // 2 KB of output rows per softmax warp
+  static constexpr int kBarOff = kOOff + 8 * 2048;
   static constexpr int kSmem = 1024 + kBarOff + 512;
   static constexpr uint32_t kIdescQK = idesc_bf16(128, kChunk, 0);
   static constexpr uint32_t kIdescPV = idesc_bf16(128, D, 1);
@@ -145,8 +144,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t p_full = s_free + 16;        // [2 halves][2 P buffers]
   const uint32_t pv_done = p_full + 32;       // [2][2]
   const uint32_t drain = pv_done + 32;        // [2]
-  const uint32_t pair = drain + 16;           // [2 halves][4 row groups]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (pair + 64 - bar));
+  const uint32_t turn = drain + 16;           // [2 halves][4 warps]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (turn + 64 - bar));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 32) {
@@ -154,13 +153,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(q_full + 8 * h, 1);
       mbar_init(q_empty + 8 * h, 2);
       mbar_init(s_full + 8 * h, 1);
-      mbar_init(s_free + 8 * h, 8);
+      mbar_init(s_free + 8 * h, 4);
       for (int u = 0; u < 2; ++u) {
-        mbar_init(p_full + 8 * (2 * h + u), 8);
+        mbar_init(p_full + 8 * (2 * h + u), 4);
         mbar_init(pv_done + 8 * (2 * h + u), 1);
       }
       mbar_init(drain + 8 * h, 1);
-      for (int w = 0; w < 4; ++w) mbar_init(pair + 8 * (4 * h + w), 2);
+      for (int w = 0; w < 4; ++w) mbar_init(turn + 8 * (4 * h + w), 1);
     }
     for (int s = 0; s < NK; ++s) {
       mbar_init(k_full + 8 * s, 1);
@@ -356,29 +355,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax + epilogue
-    const int hf = (warp - 4) >> 3;
-    const int cg = ((warp - 4) >> 2) & 1;  // columns 32 cg .. of S, D/2 cg .. of O
-    const int wr = warp & 3;               // rows 32 wr .. of the half == TMEM lanes
+    const int hf = (warp - 4) >> 2;
+    const int wr = warp & 3;        // rows 32 wr .. of the half == TMEM lanes
     const int r = wr * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(wr * 32) << 16;
-    const uint32_t tS = tmem + lane_base + hf * 64 + cg * 32;
-    const uint32_t tP = tmem + lane_base + kColP + hf * 32 + cg * 16;  // + 64 per buffer
-    const uint32_t tO = tmem + lane_base + kColO + hf * 128 + cg * (D / 2);
+    const uint32_t tS = tmem + lane_base + hf * 64;
+    const uint32_t tP = tmem + lane_base + kColP + hf * 32;  // + 64 per buffer
+    const uint32_t tO = tmem + lane_base + kColO + hf * 128;
     const float sl = p.scale_log2;
-    const uint32_t stage = sb + C::kOOff + (warp - 4) * 1024;
-    uint32_t it = 0, s_cnt = 0, swaps = 0;
+    const uint32_t stage = sb + C::kOOff + (warp - 4) * 2048;
+    uint32_t it = 0, s_cnt = 0, turns = 0;
     bool ok = true;
-    // This row's value in the warp of the other column group.  Two buffers: a
-    // warp comes back to one only after the other has arrived for the next swap.
-    auto swap = [&](float mine, float* theirs) -> bool {
-      float* buf = reinterpret_cast<float*>(smem + C::kXOff) + ((swaps & 1u) * 2 + hf) * 256 + r;
-      buf[cg * 128] = mine;
+    // In a unit of both halves the two warps of a scheduler take turns at the
+    // exponentials (half 0 first): in step they share the special-function unit
+    // there and leave it idle elsewhere (158 against 151 us as above).
+    auto turn_wait = [&]() -> bool {
+      const uint32_t n = turns++;
+      return warp_wait(turn + 8 * (4 * hf + wr), hf ? n & 1u : (n & 1u) ^ 1u, shape.err);
+    };
+    auto turn_pass = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(pair + 8 * (4 * hf + wr));
-      if (!warp_wait(pair + 8 * (4 * hf + wr), swaps & 1u, shape.err)) return false;
-      ++swaps;
-      *theirs = buf[(cg ^ 1) * 128];
-      return true;
+      if (lane == 0) mbar_arrive(turn + 8 * (4 * (hf ^ 1) + wr));
     };
     // PV k of this half: the (k / 2)-th completion of pv_done[hf][k & 1].  S of
     // chunk k + 2 is committed behind PV k, so a full S tells that the PV two
@@ -414,7 +411,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             break;
           }
           const uint32_t vb = sV + (x % NV) * C::kKV;
-          for (int c = cg * 128 + r; c < (kChunk - nk) * (D / 8); c += 256) {
+          for (int c = r; c < (kChunk - nk) * (D / 8); c += 128) {
             const int row = nk + c / (D / 8), ch = c % (D / 8);
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                              vb + (ch >> 3) * 8192 + row * 128 + (ch & 7) * 16),
@@ -424,6 +421,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           fence_proxy_async_smem();
         }
         if (!active) {
+          if (hs.both) {
+            if (!turn_wait()) {
+              ok = false;
+              break;
+            }
+            turn_pass();
+          }
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(s_free + 8 * hf);
@@ -432,33 +436,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           continue;
         }
         tc_fence_after();
-        uint32_t sr[32];
-        tmem_ld32(tS, sr);
+        uint32_t sr[2][32];
+        tmem_ld32(tS, sr[0]);
+        tmem_ld32(tS + 32, sr[1]);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free + 8 * hf);  // S is in registers
-        float x[32];
+        float x[kChunk];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(sr[k]);
+        for (int k = 0; k < kChunk; ++k) x[k] = __uint_as_float(sr[k >> 5][k & 31]);
         if (ragged) {
-          const int lim = nk - 32 * cg;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = k < lim ? x[k] : -INFINITY;
+          for (int k = 0; k < kChunk; ++k) x[k] = k < nk ? x[k] : -INFINITY;
         }
-        float mq[2];
+        float mq[4];
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          mq[a] = fmax3_nan(x[16 * a], x[16 * a + 1], x[16 * a + 2]);
+        for (int a = 0; a < 4; ++a) {
+          float v = fmax3_nan(x[16 * a], x[16 * a + 1], x[16 * a + 2]);
 #pragma unroll
-          for (int k = 3; k < 15; k += 2) mq[a] = fmax3_nan(mq[a], x[16 * a + k], x[16 * a + k + 1]);
+          for (int k = 3; k < 15; k += 2) v = fmax3_nan(v, x[16 * a + k], x[16 * a + k + 1]);
+          mq[a] = fmax3_nan(v, x[16 * a + 15], m);
         }
-        float mnew = fmax3_nan(fmax3_nan(mq[0], x[15], mq[1]), x[31], m), other;
-        if (!swap(mnew, &other)) {  // both warps of a row go by one maximum
-          ok = false;
-          break;
-        }
-        mnew = fmax3_nan(mnew, other, m);
+        const float mnew = fmax3_nan(fmax3_nan(mq[0], mq[1], mq[2]), mq[3], m);
         if (!(mnew < INFINITY)) l = NAN;  // a NaN or +inf logit makes the row NaN
         // Lazy rescale: a row moves its maximum only when it grew by more than
         // 2^8; the warp rescales together (the others by 1).  The unit's first
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             break;
           }
 #pragma unroll 1
-          for (int cc = 0; cc < D / 2; cc += 32) {
+          for (int cc = 0; cc < D; cc += 32) {
             uint32_t ov[32];
             tmem_ld32(tO + cc, ov);
             tmem_wait_ld();
@@ -489,17 +489,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         const float nm = m == -INFINITY ? 0.f : -m * sl;
         const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(nm, nm);
-        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t pk[16];
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f)};
+        uint32_t pk[32];
+        if (hs.both && !turn_wait()) {
+          ok = false;
+          break;
+        }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < 32; ++e) {
           const float2 xe = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), sl2, nm2);
           const float2 pe = make_float2(fast_exp2(xe.x), fast_exp2(xe.y));
-          acc[e & 1] = __fadd2_rn(acc[e & 1], pe);
+          acc[e & 3] = __fadd2_rn(acc[e & 3], pe);
           pk[e] = pack_bf16x2(pe.x, pe.y);
         }
-        l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-        tmem_st16(tP + (kc & 1u) * 64, pk);
+        if (hs.both) turn_pass();
+        l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y) + (acc[2].x + acc[2].y) +
+             (acc[3].x + acc[3].y);
+        tmem_st32(tP + static_cast<uint32_t>(kc & 1) * 64, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -511,13 +518,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // epilogue: this half's partial rows
       const int64_t slot = static_cast<int64_t>(blockIdx.x) + g.unit;
       const int64_t row0 = slot * kPdTcSlotRows + hf * 128;
-      float l2 = 0.f;
-      if (hs.n > 0 && !swap(l, &l2)) {
-        ok = false;
-        break;
-      }
-      l += l2;
-      if (valid && cg == 0)
+      if (valid)
         p.a.plse[row0 + rr] =
             hs.n == 0 || l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * sl) + log2f(l);
       if (hs.n == 0) continue;
@@ -528,9 +529,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.0f / l;
       if (hs.small) {
         // a few rows: each from its thread
-        float* po = p.a.po + (row0 + rr) * D + cg * (D / 2);
+        float* po = p.a.po + (row0 + rr) * D;
 #pragma unroll 1
-        for (int cc = 0; cc < D / 2; cc += 32) {
+        for (int cc = 0; cc < D; cc += 32) {
           uint32_t ov[32];
           tmem_ld32(tO + cc, ov);
           tmem_wait_ld();
@@ -543,21 +544,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       } else {
-        // 32 rows x 8 columns at a time through shared memory (row stores
+        // 32 rows x 16 columns at a time through shared memory (row stores
         // from the threads would touch 32 lines each).  Rows past the unit's
         // land in the slot's unused rows.
 #pragma unroll 1
-        for (int cc = 0; cc < D / 2; cc += 32) {
+        for (int cc = 0; cc < D; cc += 32) {
           uint32_t ov[32];
           tmem_ld32(tO + cc, ov);
           tmem_wait_ld();
 #pragma unroll
-          for (int c2 = 0; c2 < 32; c2 += 8) {
+          for (int c2 = 0; c2 < 32; c2 += 16) {
             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();  // the previous store has read the staged rows
+            // 64-byte swizzle: 16-byte chunk e of row r at e ^ (r / 2 % 4)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 32 + e * 16),
+            for (int e = 0; e < 4; ++e)
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)),
                            "f"(__uint_as_float(ov[c2 + 4 * e]) * inv),
                            "f"(__uint_as_float(ov[c2 + 4 * e + 1]) * inv),
                            "f"(__uint_as_float(ov[c2 + 4 * e + 2]) * inv),
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&tmO, stage, cg * (D / 2) + cc + c2, static_cast<int>(row0) + wr * 32);
+              tma_store_2d(&tmO, stage, cc + c2, static_cast<int>(row0) + wr * 32);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
           }
@@ -605,10 +608,10 @@ cudaError_t launch_tc(const Launch& l, const PdParams& p, std::string* why) {
   const uint64_t Hq = p.Hq;
   if (!kv_map(&k, p.Kp, s.N, s.Hkv, s.Tp, D, p.kps, &m.kh, &m.kn, why) ||
       !kv_map(&v, p.Vp, s.N, s.Hkv, s.Tp, D, p.vps, &m.vh, &m.vn, why) ||
-      !make_tmap_3d(&q, p.q, false, D, Hq, s.B, D, Hq * D, 64, s.G, 128 / s.G, true, why) ||
-      !make_tmap_3d(&qs, p.q, false, D, Hq, s.B, D, Hq * D, 64, s.G, 32 / s.G, true, why) ||
-      !make_tmap_3d(&o, p.a.po, true, D, static_cast<uint64_t>(p.a.slots) * kPdTcSlotRows, 0, D, 0, 8,
-                    32, 0, false, why))
+      !make_tmap_3d(&q, p.q, false, D, Hq, s.B, D, Hq * D, 64, s.G, 128 / s.G, 128, why) ||
+      !make_tmap_3d(&qs, p.q, false, D, Hq, s.B, D, Hq * D, 64, s.G, 32 / s.G, 128, why) ||
+      !make_tmap_3d(&o, p.a.po, true, D, static_cast<uint64_t>(p.a.slots) * kPdTcSlotRows, 0, D, 0, 16,
+                    32, 0, 64, why))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -69,7 +69,7 @@ bool make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t cols, uint64
 
 bool make_tmap_3d(CUtensorMap* map, const void* base, bool f32, uint64_t cols, uint64_t rows,
                   uint64_t n1, uint64_t row_stride, uint64_t s1, uint32_t box_cols,
-                  uint32_t box_rows, uint32_t box_n1, bool swizzle, std::string* why) {
+                  uint32_t box_rows, uint32_t box_n1, int swizzle, std::string* why) {
   auto fn = encode_fn();
   if (fn == nullptr) {
     if (why) *why = "cuTensorMapEncodeTiled is not available from the driver";
@@ -83,7 +83,7 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, bool f32, uint64_t cols, u
   CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                   n1 > 0 ? 3 : 2, const_cast<void*>(base), gdim, gstride, box, estride,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     if (why) *why = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(static_cast<int>(r));
