@@ -22,140 +22,155 @@ namespace {
 // ------------------------------------------------------------------ fp32
 //
 // Plain fp32 products on the FMA pipe: a tile of 32 query rows against chunks
-// of 64 keys held in shared memory.
+// of 32 keys held in shared memory, a thread four rows by two keys of the logits
+// and four rows by D/16 columns of the output.  Bound: with few rows HBM (a
+// chunk is 256 D bytes), with 32 the FMA pipe (2 * 32 * 32 * D products a
+// chunk).  Small chunks and CTAs, four per SM: the loads of one hide under
+// the products of the others, and a short batch still fills the SMs (one
+// chunk of 64 keys on 256 threads, two CTAs per SM: 35 us for 8 sequences over
+// 4K tokens).
 constexpr int kF32Rows = 32;
-constexpr int kF32Threads = 256;
-constexpr int kF32ChunkLog2 = 6, kF32Chunk = 1 << kF32ChunkLog2;
+constexpr int kF32Threads = 128;
+constexpr int kF32Ctas = 4;  // per SM
+constexpr int kF32ChunkLog2 = 5, kF32Chunk = 1 << kF32ChunkLog2;
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// 16 bytes into shared memory, zeros if !in (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const float* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams p) {
   constexpr int KS = D + 4, SS = kF32Chunk + 4;
+  constexpr int D4 = D / 4;
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;                           // [32][KS]
-  float* sk = sq + kF32Rows * KS;           // [64][KS]
-  float* sv = sk + kF32Chunk * KS;           // [64][D]
-  float* ss = sv + kF32Chunk * D;            // [32][SS]
+  float* sk = sq + kF32Rows * KS;           // [32][KS]
+  float* sv = sk + kF32Chunk * KS;          // [32][D]
+  float* ss = sv + kF32Chunk * D;           // [32][SS]
   __shared__ int gs[kPdMaxPrefixes + 1];
   __shared__ PdStart st;
   __shared__ uint64_t scan_sh[kF32Threads / 32];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const PdShape& shape = p.b.s;
-  if (tid < 32) pd_groups(shape, gs);
   const int key0 = tid < shape.N + shape.B ? pd_raw_keys(shape, tid) : 0;
+  if (tid < 32) pd_groups(shape, gs);
   __syncthreads();
   pd_locate<1>(shape, nullptr, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.b.plan : nullptr);
   PdWalk walk(shape, gs, st);
   PdSeg g;
   while (walk.next(g)) {
-    for (int i = tid; i < kF32Rows * (D / 4); i += kF32Threads) {
-      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < g.rows) {
-        const int row = g.row0 + r, b = row / shape.G, hd = g.h * shape.G + row % shape.G;
-        x = ld4(static_cast<const float*>(p.q) + (static_cast<int64_t>(b) * p.Hq + hd) * D + d);
-      }
-      *reinterpret_cast<float4*>(sq + r * KS + d) = x;
-    }
     const int64_t* kst = g.own ? p.ks : p.kps;
     const int64_t* vst = g.own ? p.vs : p.vps;
     const int64_t k0 = g.own ? g.b : g.n;
     const float* Kg = static_cast<const float*>(g.own ? p.K : p.Kp) + k0 * kst[0] + g.h * kst[1];
     const float* Vg = static_cast<const float*>(g.own ? p.V : p.Vp) + k0 * vst[0] + g.h * vst[1];
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[2][D / 16];
+    const float* q = static_cast<const float*>(p.q);
+    for (int i = tid; i < kF32Rows * D4; i += kF32Threads) {
+      const int r = i / D4, d = (i % D4) * 4;
+      const int row = g.row0 + r, b = row / shape.G, hd = g.h * shape.G + row % shape.G;
+      const bool in = r < g.rows;
+      copy16(smem_u32(sq + r * KS + d), in ? q + (static_cast<int64_t>(b) * p.Hq + hd) * D + d : q, in);
+    }
+    // warps whose rows are past the unit's only help with the loads
+    const bool active = (ty & ~1) * 4 < g.rows;
+    float m[4], l[4], o[4][D / 16];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 4; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) o[r][d] = 0.f;
+    }
     for (int j = g.j0; j < g.j1; ++j) {
       const int t0 = j * kF32Chunk, nk = min(kF32Chunk, g.keys - t0);
-      __syncthreads();  // the previous chunk's values have been read
-      for (int i = tid; i < kF32Chunk * (D / 4); i += kF32Threads) {
-        const int t = i / (D / 4), d = (i % (D / 4)) * 4;
-        // rows past the keys are zero: whatever the cache holds there, 0 * v stays 0
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (t < nk) {
-          x = ld4(Kg + (t0 + t) * kst[2] + d);
-          y = ld4(Vg + (t0 + t) * vst[2] + d);
-        }
-        *reinterpret_cast<float4*>(sk + t * KS + d) = x;
-        *reinterpret_cast<float4*>(sv + t * D + d) = y;
+      // rows past the keys are zero: whatever the cache holds there, 0 * v stays 0
+#pragma unroll 4
+      for (int i = tid; i < kF32Chunk * D4; i += kF32Threads) {
+        const int t = i / D4, d = (i % D4) * 4;
+        copy16(smem_u32(sk + t * KS + d), t < nk ? Kg + (t0 + t) * kst[2] + d : q, t < nk);
+        copy16(smem_u32(sv + t * D + d), t < nk ? Vg + (t0 + t) * vst[2] + d : q, t < nk);
       }
+      asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
       __syncthreads();
-      float s[2][4] = {};
+      if (active) {
+        float s[4][2] = {};
 #pragma unroll 4
-      for (int d = 0; d < D; d += 4) {
-        float4 a[2], k[4];
+        for (int d = 0; d < D; d += 4) {
+          float4 a[4], k[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) a[r] = ld4(sq + (ty * 2 + r) * KS + d);
+          for (int r = 0; r < 4; ++r) a[r] = ld4(sq + (ty * 4 + r) * KS + d);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) k[c] = ld4(sk + (tx + 16 * c) * KS + d);
+          for (int c = 0; c < 2; ++c) k[c] = ld4(sk + (tx + 16 * c) * KS + d);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+          for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            s[r][c] += a[r].x * k[c].x + a[r].y * k[c].y + a[r].z * k[c].z + a[r].w * k[c].w;
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = ty * 2 + r;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          s[r][c] = tx + 16 * c < nk ? s[r][c] * p.scale_log2 : -INFINITY;
-          mx = fmaxf(mx, s[r][c]);
-        }
-        if (g.own && p.logits && row < g.rows) {
-          float* lg = p.logits + (static_cast<int64_t>(g.unit) * shape.G + row) * p.Tl + t0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) lg[tx + 16 * c] = s[r][c];
+            for (int c = 0; c < 2; ++c)
+              s[r][c] += a[r].x * k[c].x + a[r].y * k[c].y + a[r].z * k[c].z + a[r].w * k[c].w;
         }
 #pragma unroll
-        for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn;
-        const float al = exp2f(m[r] - base);
-        float sum = 0.f;
+        for (int r = 0; r < 4; ++r) {
+          const int row = ty * 4 + r;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float e = exp2f(s[r][c] - base);
-          sum += e;
-          ss[row * SS + tx + 16 * c] = e;
-        }
-#pragma unroll
-        for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        l[r] = l[r] * al + sum;
-        m[r] = mn;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) o[r][d] *= al;
-      }
-      __syncwarp();  // a row's weights are written and read by the same half-warp
-#pragma unroll 4
-      for (int t = 0; t < kF32Chunk; ++t) {
-        float pw[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) pw[r] = ss[(ty * 2 + r) * SS + t];
-#pragma unroll
-        for (int d = 0; d < D / 64; ++d) {
-          const float4 v = ld4(sv + t * D + d * 64 + tx * 4);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            o[r][4 * d] += pw[r] * v.x;
-            o[r][4 * d + 1] += pw[r] * v.y;
-            o[r][4 * d + 2] += pw[r] * v.z;
-            o[r][4 * d + 3] += pw[r] * v.w;
+          for (int c = 0; c < 2; ++c)
+            s[r][c] = tx + 16 * c < nk ? s[r][c] * p.scale_log2 : -INFINITY;
+          if (g.own && p.logits && row < g.rows) {
+            float* lg = p.logits + (static_cast<int64_t>(g.unit) * shape.G + row) * p.Tl + t0;
+            lg[tx] = s[r][0];
+            lg[tx + 16] = s[r][1];
           }
+          float mx = fmaxf(s[r][0], s[r][1]);
+#pragma unroll
+          for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn;
+          const float al = exp2f(m[r] - base);
+          const float e0 = exp2f(s[r][0] - base), e1 = exp2f(s[r][1] - base);
+          ss[row * SS + tx] = e0;
+          ss[row * SS + tx + 16] = e1;
+          float sum = e0 + e1;
+#pragma unroll
+          for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+          l[r] = l[r] * al + sum;
+          m[r] = mn;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) o[r][d] *= al;
+        }
+        __syncwarp();  // a row's weights are written and read by the same half-warp
+#pragma unroll 2
+        for (int t = 0; t < kF32Chunk; t += 4) {
+          float4 pw[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) pw[r] = ld4(ss + (ty * 4 + r) * SS + t);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d) {
+              const float4 v = ld4(sv + (t + k) * D + d * 64 + tx * 4);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float w = k == 0 ? pw[r].x : k == 1 ? pw[r].y : k == 2 ? pw[r].z : pw[r].w;
+                o[r][4 * d] += w * v.x;
+                o[r][4 * d + 1] += w * v.y;
+                o[r][4 * d + 2] += w * v.z;
+                o[r][4 * d + 3] += w * v.w;
+              }
+            }
         }
       }
+      __syncthreads();  // the chunk, and after the last one the queries, have been read
     }
+    if (!active) continue;
     const int64_t slot = static_cast<int64_t>(blockIdx.x) + g.unit;
     const int rows = g.own ? shape.G : p.b.slot_rows;
     float* po = (g.own ? p.oo : p.b.po) + slot * rows * D;
     float* pl = (g.own ? p.olse : p.b.plse) + slot * rows;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = ty * 2 + r;
+    for (int r = 0; r < 4; ++r) {
+      const int row = ty * 4 + r;
       if (row < g.rows) {
         const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];  // a NaN stays one
 #pragma unroll
@@ -166,7 +181,6 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
         if (tx == 0) pl[row] = l[r] == 0.f ? -INFINITY : m[r] + log2f(l[r]);
       }
     }
-    __syncthreads();  // the queries have been read
   }
 }
 
@@ -201,7 +215,7 @@ struct MergeSrc {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const PdParams p, int share) {
+__global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams p, int share) {
   const PdShape& s = p.b.s;
   const int u = blockIdx.y, b = u / s.Hkv, h = u - b * s.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -416,7 +430,7 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
   s.T = T;
   Carver c{ws};
   p->a.s = p->b.s = s;
-  // fp32: one line of 32-row tiles, two CTAs per SM.  bf16: one CTA per SM for
+  // fp32: one line of 32-row tiles.  bf16: one CTA per SM for
   // the groups of many rows, and the warps for everything else.
   PdShape& a = p->a.s;
   PdShape& b = p->b.s;
@@ -444,7 +458,7 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
     p->b.slot_rows = kPdFewRows;
   } else {
     b.R = kF32Rows;
-    b.ctas = 2 * num_sms;
+    b.ctas = kF32Ctas * num_sms;
     b.workers = 1;
     b.chunk_log2 = kF32ChunkLog2;
     b.max_rows = 1 << 30;
