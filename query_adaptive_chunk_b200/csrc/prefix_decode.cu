@@ -53,15 +53,15 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
   float* sv = sk + kF32Chunk * KS;          // [32][D]
   float* ss = sv + kF32Chunk * D;           // [32][SS]
   __shared__ int gs[kPdMaxPrefixes + 1];
-  __shared__ PdStart st;
+  __shared__ PdStart st[8];
   __shared__ uint64_t scan_sh[kF32Threads / 32];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const PdShape& shape = p.b.s;
   const int key0 = tid < shape.N + shape.B ? pd_raw_keys(shape, tid) : 0;
   if (tid < 32) pd_groups(shape, gs);
   __syncthreads();
-  pd_locate<1>(shape, nullptr, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.b.plan : nullptr);
-  PdWalk walk(shape, gs, st);
+  pd_locate(p.a.s, shape, gs, key0, st, scan_sh, nullptr, blockIdx.x == 0 ? &p.b.plan : nullptr);
+  PdWalk walk(shape, gs, st[0]);
   PdSeg g;
   while (walk.next(g)) {
     const int64_t* kst = g.own ? p.ks : p.kps;
@@ -409,7 +409,7 @@ struct Carver {
 void carve_line(Carver* c, PdLine* ln, int D, int64_t units) {
   const PdShape& s = ln->s;
   ln->plan.starts = c->take<int32_t>(s.N + s.B + 2);
-  ln->plan.ubase = c->take<int32_t>(s.N + 1);
+  ln->plan.ubase = c->take<int32_t>(s.N);
   ln->plan.gsan = c->take<int32_t>(s.N + 1);
   ln->plan.group = c->take<int32_t>(s.B);
   ln->slots = units > 0 ? s.ctas * s.workers + units : 0;
@@ -438,24 +438,23 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
   b.min_rows = 1;
   if (bf16) {
     a.R = pd_tc_rows(G);
-    a.ctas = N > 0 && Tp > 0 && rows > kPdFewRows ? num_sms : 0;
+    a.ctas = N > 0 && Tp > 0 && rows > pd_few_rows(G) ? num_sms : 0;
     a.workers = 1;
-    a.first = 1;
     // a chunk's time in 16-key steps of the warps: its bytes, and half as much
     // again where both halves' rows are at work (groups taken as of equal size)
     a.cost = 4.f * (N > 0 && rows / N > a.R / 2 ? 1.5f : 1.f);
     b.cost = 1.f;
     a.chunk_log2 = kPdTcChunkLog2;
-    a.min_rows = kPdFewRows + 1;
+    a.min_rows = pd_few_rows(G) + 1;
     a.max_rows = 1 << 30;
     p->a.halves = 2;
     p->a.slot_rows = kPdTcSlotRows;
-    b.R = kPdFewRows;
+    b.R = pd_few_rows(G);
     b.ctas = num_sms;
     b.workers = kPdWarps;
     b.chunk_log2 = kPdWarpChunkLog2;
-    b.max_rows = kPdFewRows;
-    p->b.slot_rows = kPdFewRows;
+    b.max_rows = b.R;
+    p->b.slot_rows = b.R;
   } else {
     b.R = kF32Rows;
     b.ctas = kF32Ctas * num_sms;
@@ -465,6 +464,8 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
     p->b.slot_rows = kF32Rows;
   }
   p->b.halves = 1;
+  a.inv_R = bf16 ? 1.f / a.R : 0.f;
+  b.inv_R = 1.f / b.R;
   // tiles of all groups: at most rows / R + N
   if (a.ctas > 0) carve_line(&c, &p->a, D, Hkv * (rows / a.R + N));
   carve_line(&c, &p->b, D, N > 0 && Tp > 0 ? Hkv * (bf16 ? N : rows / b.R + N) : 0);
@@ -550,8 +551,7 @@ cudaError_t launch_prefix_decode(const Launch& l, const PrefixDecodeArgs& a, std
   p.decay = a.decay;
   cudaError_t e = cudaSuccess;
   if (a.bf16) {
-    if (p.a.s.ctas > 0) e = launch_attend_tc(l, p, a.D, why);
-    if (e == cudaSuccess) e = launch_attend_warp(l, p, a.D);
+    e = launch_attend_bf16(l, p, a.D, why);
   } else {
     e = a.D == 128 ? launch_attend_f32<128>(l, p) : launch_attend_f32<64>(l, p);
   }

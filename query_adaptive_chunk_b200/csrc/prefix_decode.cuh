@@ -8,12 +8,12 @@ namespace csa {
 constexpr float kPdLog2e = 1.4426950408889634f;
 constexpr float kPdLn2 = 0.6931471805599453f;
 
-// bf16: groups of more rows than this go to the tensor-memory kernel
-// (prefix_decode_tc.cu), the others and the own units to the warps
-// (prefix_decode_warp.cu).
-constexpr int kPdFewRows = 16;
+// bf16: groups of more rows than line b's tile are line a (prefix_tc.cuh), the
+// others and the own units line b (prefix_warp.cuh), whose tile is the G rows of
+// an own unit rounded up to eights.  fp32 has line b alone.
+inline int pd_few_rows(int G) { return G <= 8 ? 8 : 16; }
 
-// One kernel's line of units and where its partials go.  A prefix unit's slot
+// A line of units and where its partials go.  A prefix unit's slot
 // holds `slot_rows` rows, an own unit's G.  With halves = 2 row r of a tile
 // lies at (r / (R/2)) * slot_rows/2 + r % (R/2), and a unit of at most R / 2
 // rows is split once more inside its CTA: even chunks' rows in the slot's first
@@ -43,15 +43,12 @@ struct PdParams {
   float decay;
 };
 
-// prefix_decode_tc.cu: line a.
-int pd_tc_rows(int G);  // query rows per tile
+// prefix_decode_bf16.cu
+int pd_tc_rows(int G);  // query rows per tile of line a
 constexpr int kPdTcSlotRows = 256;
 constexpr int kPdTcChunkLog2 = 6;
-cudaError_t launch_attend_tc(const Launch& l, const PdParams& p, int D, std::string* why);
-
-// prefix_decode_warp.cu: line b of bf16.
-constexpr int kPdWarps = 8;
+constexpr int kPdWarps = 8;  // warps of a CTA on line b
 constexpr int kPdWarpChunkLog2 = 4;
-cudaError_t launch_attend_warp(const Launch& l, const PdParams& p, int D);
+cudaError_t launch_attend_bf16(const Launch& l, const PdParams& p, int D, std::string* why);
 
 }  // namespace csa

@@ -1,5 +1,5 @@
-// Prefix attention of the shared-prefix decode (bf16, groups of more than
-// kPdFewRows query rows) on the 5th-generation tensor cores (tcgen05,
+// Prefix attention of the shared-prefix decode (bf16, groups of more query rows
+// than line b takes) on the 5th-generation tensor cores (tcgen05,
 // accumulators in tensor memory).
 //
 // Work unit: up to R <= 256 query rows against a run of keys (prefix_work.cuh),
@@ -35,7 +35,7 @@
 // (1 owns the tensor memory), 3 the queries (TMA; two 128-row slots, so
 // that the next small unit's rows arrive early), 4-7 and 8-11 softmax and
 // epilogue of half 0 and 1.  Every wait is bounded.
-#include <algorithm>
+#pragma once
 
 #include "prefix_decode.cuh"
 #include "tcgen05.cuh"
@@ -118,37 +118,34 @@ __device__ __forceinline__ HalfSeg half_seg(const PdSeg& g, int hf, int rh, int 
   return s;
 }
 
+// Addresses of the barriers (shared) and the places of the tensor memory's
+// address.
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1)
-    attend_tc_kernel(const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ CUtensorMap tmQ,
-                     const __grid_constant__ CUtensorMap tmQs,
-                     const __grid_constant__ CUtensorMap tmO, const TcMaps mp, const PdParams p) {
-  using C = TcCfg<D>;
-  constexpr int NK = C::kNK, NV = C::kNV;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  __shared__ int gs[kPdMaxPrefixes + 1];
-  __shared__ PdStart st;
-  __shared__ uint64_t scan_sh[kTcThreads / 32];
-  const uint32_t sb = smem_u32(smem);
-  const uint32_t sQ = sb + C::kQOff, sK = sb + C::kKOff, sV = sb + C::kVOff, bar = sb + C::kBarOff;
-  const uint32_t q_full = bar, q_empty = bar + 16;  // [2 slots] each
-  const uint32_t k_full = bar + 32, k_empty = k_full + 8 * NK;
-  const uint32_t v_full = k_empty + 8 * NK, v_empty = v_full + 8 * NV;
-  const uint32_t s_full = v_empty + 8 * NV;  // [2 halves]
-  const uint32_t s_free = s_full + 16;        // [2]
-  const uint32_t p_full = s_free + 16;        // [2 halves][2 P buffers]
-  const uint32_t pv_done = p_full + 32;       // [2][2]
-  const uint32_t drain = pv_done + 32;        // [2]
-  const uint32_t turn = drain + 16;           // [2 halves][4 warps]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (turn + 64 - bar));
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 32) {
+struct TcBars {
+  static constexpr int NK = TcCfg<D>::kNK, NV = TcCfg<D>::kNV;
+  uint32_t q_full, q_empty;    // [2 slots] each
+  uint32_t k_full, k_empty, v_full, v_empty;
+  uint32_t s_full, s_free;     // [2 halves]
+  uint32_t p_full, pv_done;    // [2 halves][2 P buffers]
+  uint32_t drain;              // [2]
+  uint32_t turn;               // [2 halves][4 warps]
+  uint32_t end;
+  __device__ __forceinline__ explicit TcBars(uint32_t bar) {
+    q_full = bar;
+    q_empty = bar + 16;
+    k_full = bar + 32;
+    k_empty = k_full + 8 * NK;
+    v_full = k_empty + 8 * NK;
+    v_empty = v_full + 8 * NV;
+    s_full = v_empty + 8 * NV;
+    s_free = s_full + 16;
+    p_full = s_free + 16;
+    pv_done = p_full + 32;
+    drain = pv_done + 32;
+    turn = drain + 16;
+    end = turn + 64;
+  }
+  __device__ __forceinline__ void init() const {  // one thread
     for (int h = 0; h < 2; ++h) {
       mbar_init(q_full + 8 * h, 1);
       mbar_init(q_empty + 8 * h, 2);
@@ -171,21 +168,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     fence_barrier_init();
   }
+};
+
+// A CTA of line a: worker `block`.  The barriers are set up and the tensor
+// memory is allocated by warp 1, which frees it after this.
+template <int D>
+__device__ __forceinline__ void attend_tc(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                          const CUtensorMap& tmQ, const CUtensorMap& tmQs,
+                                          const CUtensorMap& tmO, const TcMaps& mp,
+                                          const PdParams& p, uint8_t* smem, const TcBars<D>& bars,
+                                          uint32_t tmem, const int* gs, const PdStart& st,
+                                          int block) {
+  using C = TcCfg<D>;
+  constexpr int NK = C::kNK, NV = C::kNV;
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t sQ = sb + C::kQOff, sK = sb + C::kKOff, sV = sb + C::kVOff;
+  const uint32_t q_full = bars.q_full, q_empty = bars.q_empty;
+  const uint32_t k_full = bars.k_full, k_empty = bars.k_empty;
+  const uint32_t v_full = bars.v_full, v_empty = bars.v_empty;
+  const uint32_t s_full = bars.s_full, s_free = bars.s_free;
+  const uint32_t p_full = bars.p_full, pv_done = bars.pv_done;
+  const uint32_t drain = bars.drain, turn = bars.turn;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PdShape& shape = p.a.s;
-  const int items = shape.N + shape.B;
-  const int key0 = static_cast<int>(threadIdx.x) < items ? pd_raw_keys(shape, threadIdx.x) : 0;
-  if (warp == 0) pd_groups(shape, gs);
-  if (threadIdx.x == 96) {
-    prefetch_tensormap(&tmQ);
-    prefetch_tensormap(&tmK);
-    prefetch_tensormap(&tmV);
-  }
-  if (warp == 1) tmem_alloc<512>(tmem_slot);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  pd_locate<1>(shape, &p.b.s, gs, key0, &st, scan_sh, blockIdx.x == 0 ? &p.a.plan : nullptr);
   const int rh = shape.R / 2;
 
   PdWalk walk(shape, gs, st);
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       it += g.j1 - g.j0;
       if (!active) continue;
       // epilogue: this half's partial rows
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) + g.unit;
+      const int64_t slot = static_cast<int64_t>(block) + g.unit;
       const int64_t row0 = slot * kPdTcSlotRows + hf * 128;
       if (valid)
         p.a.plse[row0 + rr] =
@@ -585,49 +590,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc<512>(tmem);
-}
-
-// A tensor map of [n0, n1, rows, D]; a dimension of one entry, or of stride 0
-// (the same rows for all), becomes one entry with multiplier 0.
-bool kv_map(CUtensorMap* map, const void* base, int64_t n0, int64_t n1, int64_t rows, int D,
-            const int64_t* st, int* m1, int* m0, std::string* why) {
-  *m1 = n1 > 1 && st[1] != 0;
-  *m0 = n0 > 1 && st[0] != 0;
-  const uint64_t rs = rows > 1 ? st[2] : D;
-  return make_tmap_bf16_4d(map, base, D, rows, *m1 ? n1 : 1, *m0 ? n0 : 1, rs, *m1 ? st[1] : D,
-                           *m0 ? st[0] : D, kChunk, 64, why);
-}
-
-template <int D>
-cudaError_t launch_tc(const Launch& l, const PdParams& p, std::string* why) {
-  const PdShape& s = p.a.s;
-  CUtensorMap k, v, q, qs, o;
-  TcMaps m{};
-  m.few = 32 / s.G * s.G;
-  const uint64_t Hq = p.Hq;
-  if (!kv_map(&k, p.Kp, s.N, s.Hkv, s.Tp, D, p.kps, &m.kh, &m.kn, why) ||
-      !kv_map(&v, p.Vp, s.N, s.Hkv, s.Tp, D, p.vps, &m.vh, &m.vn, why) ||
-      !make_tmap_3d(&q, p.q, false, D, Hq, s.B, D, Hq * D, 64, s.G, 128 / s.G, 128, why) ||
-      !make_tmap_3d(&qs, p.q, false, D, Hq, s.B, D, Hq * D, 64, s.G, 32 / s.G, 128, why) ||
-      !make_tmap_3d(&o, p.a.po, true, D, static_cast<uint64_t>(p.a.slots) * kPdTcSlotRows, 0, D, 0, 16,
-                    32, 0, 64, why))
-    return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       TcCfg<D>::kSmem);
-  if (e != cudaSuccess) return e;
-  attend_tc_kernel<D><<<s.ctas, kTcThreads, TcCfg<D>::kSmem, l.stream>>>(k, v, q, qs, o, m, p);
-  return cudaGetLastError();
 }
 
 }  // namespace
-
-// A tile's halves hold whole sequences, at most 128 rows.
-int pd_tc_rows(int G) { return 2 * (128 / G * G); }
-
-cudaError_t launch_attend_tc(const Launch& l, const PdParams& p, int D, std::string* why) {
-  return D == 128 ? launch_tc<128>(l, p, why) : launch_tc<64>(l, p, why);
-}
-
 }  // namespace csa

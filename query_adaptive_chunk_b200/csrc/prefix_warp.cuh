@@ -1,4 +1,4 @@
-// Own caches, and prefixes of at most kPdFewRows query rows, of the
+// Own caches, and prefixes of at most 8 (16 for G > 8) query rows, of the
 // shared-prefix decode (bf16).
 //
 // Every warp works by itself: it takes its share of the line (prefix_work.cuh)
@@ -18,14 +18,13 @@
 // instructions; with 192 KB in flight per SM the loads run ahead of the
 // products.  Rows past a unit's keys are filled with zeros by the copy itself,
 // so what the cache holds there never enters a product.
-#include <algorithm>
+#pragma once
 
 #include "prefix_decode.cuh"
 
 namespace csa {
 namespace {
 
-constexpr int kWThreads = kPdWarps * 32;
 constexpr int kStep = 1 << kPdWarpChunkLog2;  // 16 keys
 constexpr float kWRescaleLog2 = 8.0f;
 
@@ -51,22 +50,13 @@ __device__ __forceinline__ uint32_t cell(int r, int c) {
   return static_cast<uint32_t>(r * D * 2 + ((c ^ (r & 7)) << 4));
 }
 
+// One of the kPdWarps warps of CTA `block` of line b; `smem` is the warps' rings.
 template <int D, int NT>
-__global__ void __launch_bounds__(kWThreads, 1) attend_warp_kernel(const PdParams p) {
+__device__ __forceinline__ void attend_warp(const PdParams& p, uint8_t* smem, const int* gs,
+                                            const PdStart* st, int block) {
   using C = WCfg<D>;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int gs[kPdMaxPrefixes + 1];
-  __shared__ PdStart st[kPdWarps];
-  __shared__ uint64_t scan_sh[kPdWarps];
   const PdShape& shape = p.b.s;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int key0 = tid < shape.N + shape.B ? pd_raw_keys(shape, tid) : 0;
-  if (warp == 0) pd_groups(shape, gs);
-  __syncthreads();
-  pd_locate<kPdWarps>(shape, p.a.s.ctas > 0 ? &p.a.s : nullptr, gs, key0, st, scan_sh,
-                      blockIdx.x == 0 ? &p.b.plan : nullptr);
-
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
   const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_normal();
   // ---- loads: a walk of its own, kStages - 1 steps ahead
@@ -256,8 +246,8 @@ __global__ void __launch_bounds__(kWThreads, 1) attend_warp_kernel(const PdParam
       }
     }
     // ---- the unit's share is done: its partial rows
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) * kPdWarps + warp + g.unit;
-    const int64_t row0 = slot * (g.own ? shape.G : kPdFewRows);
+    const int64_t slot = static_cast<int64_t>(block) * kPdWarps + warp + g.unit;
+    const int64_t row0 = slot * (g.own ? shape.G : shape.R);
     float* po = (g.own ? p.oo : p.b.po) + row0 * D;
     float* pl = (g.own ? p.olse : p.b.plse) + row0;
 #pragma unroll
@@ -281,36 +271,7 @@ __global__ void __launch_bounds__(kWThreads, 1) attend_warp_kernel(const PdParam
       }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  // the merge behind this kernel also reads what the one before it wrote
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-template <int D, int NT>
-cudaError_t launch_w(const Launch& l, const PdParams& p) {
-  constexpr int smem = WCfg<D>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(attend_warp_kernel<D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.b.s.ctas));
-  cfg.blockDim = dim3(kWThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = l.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.a.s.ctas > 0 ? 1 : 0;  // beside line a's kernel, on the SMs it leaves
-  return cudaLaunchKernelEx(&cfg, attend_warp_kernel<D, NT>, p);
 }
 
 }  // namespace
-
-cudaError_t launch_attend_warp(const Launch& l, const PdParams& p, int D) {
-  // rows of a unit: G for own ones, up to kPdFewRows for a prefix's
-  const bool two = p.b.s.G > 8 || (p.b.s.N > 0 && p.b.s.Tp > 0);
-  if (D == 128) return two ? launch_w<128, 2>(l, p) : launch_w<128, 1>(l, p);
-  return two ? launch_w<64, 2>(l, p) : launch_w<64, 1>(l, p);
-}
-
 }  // namespace csa

@@ -5,17 +5,18 @@
 //   prefix units (n, h, tile): the queries of up to R rows of the sequences of
 //     group n (row = sequence * G + head of the group) against prefix n;
 //   own units (b, h): the G query heads of one sequence against its own cache.
-// Units go to one of two lines, each with a kernel, by their kind and by their
-// group's rows; the two kernels run side by side, each on the share of the
-// CTAs (one per SM) that its keys are of all, found on the device (one after
-// the other, the second's start-up would add to the first's).  A unit's keys
-// are cut into chunks.  All chunks of a line's units lie end to end (prefixes
-// first; within a prefix by head, then row tile; own units by sequence, then
-// head) and worker c (a CTA, or a warp) of P takes chunks [W c / P, W (c + 1) /
-// P): every SM streams the same number of keys whatever the lengths.  A worker that holds any of unit i's chunks writes
-// one partial (normalised rows and their log2-sum-exp) to slot c + i: the
-// pairs (c, i) met along the line grow by one in c or in i at a time, so slots
-// are distinct and number at most P + units.
+// Units go to one of two lines by their kind and by their group's rows.  The
+// lines run side by side in one launch, each on the share of the CTAs (one per
+// SM) that its keys are of all (as two launches, the second's CTAs wait for SMs
+// at both ends: 42 against 32 us for 32 sequences over 8K tokens).  A unit's
+// keys are cut into chunks.  All chunks of a line's units lie end to end
+// (prefixes first; within a prefix by head, then row tile; own units by
+// sequence, then head) and worker c (a CTA, or a warp) of P takes chunks
+// [W c / P, W (c + 1) / P): every SM streams the same number of keys whatever the
+// lengths.  A worker that holds any of unit i's chunks writes one partial
+// (normalised rows and their log2-sum-exp) to slot c + i: the pairs (c, i) met
+// along the line grow by one in c or in i at a time, so slots are distinct
+// and number at most P + units.
 #pragma once
 
 #include "internal.h"
@@ -37,12 +38,12 @@ __device__ __forceinline__ int pd_clamp(int v, int64_t hi, const DevErr& e) {
 struct PdShape {
   int B, Hkv, G, N;
   int R;                       // query rows per tile
-  int ctas;                    // CTAs that both lines share (0: no such line)
-  int workers;                 // workers per CTA
+  float inv_R;
+  int ctas;                    // CTAs that the lines share (0: no such line)
+  int workers;                 // workers per CTA, at most 8
   int chunk_log2;              // keys per chunk
   int min_rows, max_rows;      // prefix units of groups of so many rows
   int own;                     // own units too
-  int first;                   // the line launched first
   float cost;                  // of a chunk, relative to the other line's
   int64_t Tp, T;
   const int32_t* prefix_len;   // [N] or null: Tp
@@ -74,7 +75,10 @@ __device__ __forceinline__ int pd_chunks(const PdShape& s, int keys) {
 // Row tiles of a group of `seqs` sequences (0: the group is not on this line).
 __device__ __forceinline__ int pd_tiles(const PdShape& s, int seqs) {
   const int rows = seqs * s.G;
-  return rows < s.min_rows || rows > s.max_rows ? 0 : (rows + s.R - 1) / s.R;
+  // ceil(rows / R): rows < 2^20, so that the product is within 1 / 2R of it
+  return rows < s.min_rows || rows > s.max_rows
+             ? 0
+             : static_cast<int>((static_cast<float>(rows + s.R) - 0.5f) * s.inv_R);
 }
 
 // gs[0 .. N]: the groups' bounds, clamped to [0, B] and made non-decreasing
@@ -114,9 +118,9 @@ struct PdStart {
 // What the merge needs to find a unit's partials, written by one CTA.
 struct PdPlan {
   int32_t* starts;  // [N + B + 2] first chunk of each item, then W, then P
-  int32_t* ubase;   // [N + 1] first unit of each prefix
-  int32_t* gsan;    // [N + 1] the sanitised group bounds
-  int32_t* group;   // [B] each sequence's prefix, or -1
+  int32_t* ubase;   // [N] first unit of each prefix
+  int32_t* gsan;    // [N + 1] the sanitised group bounds (line b's plan)
+  int32_t* group;   // [B] each sequence's prefix, or -1 (line b's plan)
 };
 
 // Exclusive prefix sum over the block of two counts packed in 64 bits, one
@@ -148,115 +152,125 @@ __device__ __forceinline__ int pd_cut(int W, int c, int P) {
   return q * c + (W - q * P) * c / P;
 }
 
-// Block-wide: fills st[0 .. NW - 1] (shared), the places of the block's NW
-// workers on line `me`; `other` is the line beside it (null: none).  `gs`
-// (shared) is filled by pd_groups before a barrier; key0 = pd_raw_keys of item
-// threadIdx.x, loaded before that barrier (any value for threads past the
-// items).
-template <int NW>
-__device__ __forceinline__ void pd_locate(const PdShape& me, const PdShape* other, const int* gs,
-                                          int key0, PdStart* st, uint64_t* scan_sh,
-                                          const PdPlan* plan) {
-  const int items = me.N + me.B, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31;
+// What a CTA works on.
+struct PdPlace {
+  int line;   // 0: a, 1: b
+  int block;  // its number on that line
+};
+
+// Block-wide: the CTA's line, and st[0 .. 7] (shared), the places of its
+// workers there.  `gs` (shared) is filled by pd_groups before a barrier; key0 =
+// pd_raw_keys of item threadIdx.x, loaded before that barrier (any value for
+// threads past the items).  One CTA passes plans to write.
+__device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b, const int* gs,
+                                             int key0, PdStart* st, uint64_t* scan_sh,
+                                             const PdPlan* plan_a, const PdPlan* plan_b) {
+  const int items = b.N + b.B, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31;
+  const bool two = a.ctas > 0;
   auto units = [&](const PdShape& s, int i) -> int {
     return i < s.N ? pd_tiles(s, gs[i + 1] - gs[i]) * s.Hkv : s.own ? s.Hkv : 0;
   };
-  // chunks of item i on this line and, in the high half, the cost of both lines' shares
-  // of it: 16 keys' loads are 1, times 3/2 where both halves' rows are at work
-  auto weigh = [&](int i, int raw, int* mine) -> uint64_t {
-    *mine = 0;
+  // chunks of item i: line a in the high half, line b in the low one
+  auto weigh = [&](int i, int raw) -> uint64_t {
     if (i >= items) return 0;
-    const int keys = pd_clamp(raw, i < me.N ? me.Tp : me.T, me.err);
-    *mine = units(me, i) * pd_chunks(me, keys);
-    return static_cast<uint64_t>(static_cast<uint32_t>(*mine));
+    const int keys = pd_clamp(raw, i < b.N ? b.Tp : b.T, b.err);
+    const uint32_t nb = units(b, i) * pd_chunks(b, keys);
+    const uint32_t na = two && i < b.N ? units(a, i) * pd_chunks(a, keys) : 0;
+    return static_cast<uint64_t>(na) << 32 | nb;
   };
-  auto cost = [&](int i, int raw) -> uint64_t {  // of the other line's share, in its chunks
-    if (other == nullptr || i >= items) return 0;
-    const int keys = pd_clamp(raw, i < me.N ? me.Tp : me.T, me.err);
-    return static_cast<uint64_t>(units(*other, i) * pd_chunks(*other, keys)) << 32;
-  };
-  auto raw_of = [&](int i) { return i < items ? pd_raw_keys(me, i) : 0; };
-  if (tid < NW) st[tid].left = 0;
-  uint64_t total = 0, ex = 0;
-  int mine = 0;
+  auto raw_of = [&](int i) { return i < items ? pd_raw_keys(b, i) : 0; };
+  if (tid < 8) st[tid].left = 0;
+  uint64_t total = 0, v = 0, ex = 0;
   const bool one = items <= nt;  // one item per thread
   if (one) {
-    const uint64_t v = weigh(tid, key0, &mine) + cost(tid, key0);
+    v = weigh(tid, key0);
     ex = pd_scan(v, scan_sh, &total);
   } else {
     for (int i0 = 0; i0 < items; i0 += nt) {
-      const int i = i0 + tid, raw = raw_of(i);
-      const uint64_t v = weigh(i, raw, &mine) + cost(i, raw);
+      const int i = i0 + tid;
       uint64_t tot;
-      pd_scan(v, scan_sh, &tot);
+      pd_scan(weigh(i, raw_of(i)), scan_sh, &tot);
       total += tot;
       __syncthreads();  // scan_sh is used again
     }
   }
-  const int W = static_cast<int>(total & 0xffffffffu);
-  // this line's CTAs: its share of the keys, at least one for each line with work
-  int ctas = me.ctas;
-  const uint64_t wo = total >> 32;
-  if (wo > 0) {
-    const float cm = static_cast<float>(W) * me.cost, co = static_cast<float>(wo) * other->cost;
-    const int a = max(1, min(me.ctas - 1, __float2int_rn(me.ctas * (me.first ? cm : co) / (cm + co))));
-    ctas = W == 0 ? 1 : me.first ? a : me.ctas - a;
+  const int Wa = static_cast<int>(total >> 32), Wb = static_cast<int>(total & 0xffffffffu);
+  // line a's CTAs: its share of the keys, at least one for each line with work
+  int na = 0;
+  if (Wa > 0) {
+    const float ca = Wa * a.cost, cb = Wb * b.cost;
+    na = Wb == 0 ? b.ctas : max(1, min(b.ctas - 1, __float2int_rn(b.ctas * ca / (ca + cb))));
   }
-  const int P = max(1, min(ctas * me.workers, W));  // each worker that takes part has a chunk
-  const int w0 = static_cast<int>(blockIdx.x) * NW;
-  const int c0 = min(P, w0 + min(lane, NW));  // lane k: where worker w0 + k starts
-  const int x_lane = pd_cut(W, c0, P);
-  auto place = [&](int i, int e, int n) {  // chunks [e, e + n) are item i's
+  // each worker that takes part has a chunk
+  const int Pa = max(1, min(na, Wa)), Pb = max(1, min((b.ctas - na) * b.workers, Wb));
+  const bool on_a = static_cast<int>(blockIdx.x) < na;
+  const PdShape& me = on_a ? a : b;
+  const int block = static_cast<int>(blockIdx.x) - (on_a ? 0 : na);
+  const int W = on_a ? Wa : Wb, P = on_a ? Pa : Pb, nw = me.workers;
+  const int x_lane = pd_cut(W, min(P, block * nw + min(lane, nw)), P);  // lane k: worker k's start
+  auto place = [&](int i, uint64_t at, uint64_t mine) {
+    const int e = static_cast<int>(on_a ? at >> 32 : at & 0xffffffffu);
+    const int n = static_cast<int>(on_a ? mine >> 32 : mine & 0xffffffffu);
 #pragma unroll 1
-    for (int k = 0; k < NW; ++k) {
+    for (int k = 0; k < nw; ++k) {
       const int x0 = __shfl_sync(0xffffffffu, x_lane, k), x1 = __shfl_sync(0xffffffffu, x_lane, k + 1);
-      if (x1 > x0 && x0 >= e && x0 < e + n) {
+      if (x1 > x0 && x0 >= e && x0 < e + n) {  // chunks [e, e + n) are item i's
         st[k].left = x1 - x0;
         st[k].item = i;
         st[k].off = x0 - e;
         int before = 0;
-        for (int m = 0; m < min(i, me.N); ++m) before += units(me, m);
+        if (i < me.N)
+          for (int m = 0; m < i; ++m) before += units(me, m);
         st[k].unit0 = before;
       }
     }
   };
+  auto write = [&](int i, uint64_t at) {
+    if (i >= items) return;
+    if (plan_a) plan_a->starts[i] = static_cast<int>(at >> 32);
+    if (plan_b) plan_b->starts[i] = static_cast<int>(at & 0xffffffffu);
+  };
   if (one) {
-    const int e = static_cast<int>(ex & 0xffffffffu);
-    place(tid, e, mine);
-    if (plan && tid < items) plan->starts[tid] = e;
+    place(tid, ex, v);
+    write(tid, ex);
   } else {
-    int run = 0;
+    uint64_t run = 0;
     for (int i0 = 0; i0 < items; i0 += nt) {
       const int i = i0 + tid;
       uint64_t tot;
-      const uint64_t v = weigh(i, raw_of(i), &mine);
-      const int e = run + static_cast<int>(pd_scan(v, scan_sh, &tot));
-      place(i, e, mine);
-      if (plan && i < items) plan->starts[i] = e;
-      run += static_cast<int>(tot);
+      const uint64_t w = weigh(i, raw_of(i));
+      const uint64_t at = run + pd_scan(w, scan_sh, &tot);
+      place(i, at, w);
+      write(i, at);
+      run += tot;
       __syncthreads();
     }
   }
-  if (plan) {
+  auto finish = [&](const PdShape& s, const PdPlan* plan, int Wl, int Pl) {
+    if (plan == nullptr) return;
     if (tid == 0) {
-      plan->starts[items] = W;
-      plan->starts[items + 1] = P;
+      plan->starts[items] = Wl;
+      plan->starts[items + 1] = Pl;
       int u = 0;
-      for (int n = 0; n < me.N; ++n) {
+      for (int n = 0; n < s.N; ++n) {
         plan->ubase[n] = u;
-        u += units(me, n);
+        u += units(s, n);
       }
-      plan->ubase[me.N] = u;
     }
-    if (me.N > 0 && tid <= me.N) plan->gsan[tid] = gs[tid];
-    for (int b = tid; b < me.B; b += nt) {
+  };
+  finish(a, plan_a, Wa, Pa);
+  finish(b, plan_b, Wb, Pb);
+  if (plan_b) {
+    if (b.N > 0 && tid <= b.N) plan_b->gsan[tid] = gs[tid];
+    for (int q = tid; q < b.B; q += nt) {
       int g = -1;
-      for (int n = 0; n < me.N; ++n)
-        if (gs[n] <= b && b < gs[n + 1]) g = n;
-      plan->group[b] = g;
+      for (int n = 0; n < b.N; ++n)
+        if (gs[n] <= q && q < gs[n + 1]) g = n;
+      plan_b->group[q] = g;
     }
   }
   __syncthreads();
+  return PdPlace{on_a ? 0 : 1, block};
 }
 
 // One worker's share of one unit.
