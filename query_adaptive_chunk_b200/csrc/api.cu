@@ -1296,8 +1296,8 @@ csa_status prefix_sizes(csa_dtype dtype, int B, int Hq, int Hkv, int D, int N, i
   // the chunks of all units are numbered with 32 bits (16 keys and row tiles
   // of 32 at least)
   const int64_t U = static_cast<int64_t>(B) * Hkv;
-  const int64_t own = U * ((T + 15) / 16);
-  const int64_t pre = N == 0 ? 0 : (U * (Hq / Hkv) / 32 + static_cast<int64_t>(N) * Hkv) * ((Tp + 15) / 16);
+  const int64_t own = U * ((T + 15) / 16 + 8);
+  const int64_t pre = N == 0 ? 0 : (U * (Hq / Hkv) / 32 + static_cast<int64_t>(N) * Hkv) * ((Tp + 15) / 16 + 8);
   CSA_SUPPORT(own < 2147483648LL && pre < 2147483648LL - own,
               "too many keys in all (chunks of 16 keys, times row tiles, must be < 2^31)");
   return CSA_OK;

@@ -180,7 +180,7 @@ __device__ __forceinline__ int source_len(const int32_t* len, int b, int64_t S, 
 template <int CS>
 __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const CompressParams p) {
   if (CS > 1) cluster_arrive_relaxed();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_next();  // the copy
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ unsigned int hw[kCmpThreads / 32][256];  // a histogram per warp: no contention between them
   __shared__ unsigned int hc[256], gc[256];
@@ -380,7 +380,7 @@ struct CopyParams {
 };
 
 __global__ void __launch_bounds__(kCopyThreads) compress_copy_kernel(const CopyParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the row numbers are written
+  pdl_wait();  // the row numbers are written
   const CacheArgs& d = p.dst;
   const int u = blockIdx.y, b = u / d.Hkv, h = u - b * d.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -509,17 +509,9 @@ cudaError_t launch_cache_compress(const Launch& l, const CacheArgs& dst, const C
   p.err = l.err;
   const int64_t most = std::min<int64_t>(dst.budget, s.S);
   const int per_block = kCopyThreads / 32 * kCopyRows;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, (most + per_block - 1) / per_block)),
-                     static_cast<unsigned>(U));
-  cfg.blockDim = dim3(kCopyThreads);
-  cfg.stream = l.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, compress_copy_kernel, p);
+  const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, (most + per_block - 1) / per_block)),
+                  static_cast<unsigned>(U));
+  return launch_behind(compress_copy_kernel, grid, dim3(kCopyThreads), 0, l.stream, p);
 }
 
 }  // namespace csa

@@ -176,6 +176,15 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// ------------------------------------------------------------------ dependent launch
+
+// The kernels before this one on the stream are complete, their writes visible.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel on the stream may start once every CTA has come here.
+__device__ __forceinline__ void pdl_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ clusters
 
 // Cluster barrier halves: every thread of every CTA of the cluster arrives

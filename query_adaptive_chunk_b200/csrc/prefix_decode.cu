@@ -33,6 +33,7 @@ constexpr int kF32Rows = 32;
 constexpr int kF32Threads = 128;
 constexpr int kF32Ctas = 4;  // per SM
 constexpr int kF32ChunkLog2 = 5, kF32Chunk = 1 << kF32ChunkLog2;
+constexpr int kF32Lead = 1;  // a unit's queries and partials, in chunks' time
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
@@ -57,6 +58,7 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
   __shared__ uint64_t scan_sh[kF32Threads / 32];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const PdShape& shape = p.b.s;
+  pdl_next();  // the merge
   const int key0 = tid < shape.N + shape.B ? pd_raw_keys(shape, tid) : 0;
   if (tid < 32) pd_groups(shape, gs);
   __syncthreads();
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
   __shared__ float lse2[kMaxG];
   __shared__ MergeSrc src[kMaxG];
   __shared__ float4 red[kMergeThreads];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's partials
+  pdl_wait();  // the attention kernel's partials
   for (int g = warp; g < s.G; g += kMergeThreads / 32) {
     MergeSrc m{};
     const int W = p.b.plan.starts[s.N + s.B], P = p.b.plan.starts[s.N + s.B + 1];
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
         const int tile = r / R;
         r -= tile * R;
         const int rows = min(R, seqs * s.G - tile * R);
-        const int ui = h * tiles + tile, x = x_pre + ui * c;
+        const int ui = h * tiles + tile, x = x_pre + ui * (c + ln.s.lead) + ln.s.lead;
         const int c0 = pd_worker_of(x, Wl, Pl), c1 = pd_worker_of(x + c - 1, Wl, Pl);
         if (ln.halves == 2) {
           const int rh = R / 2;
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
     }
     const int c = pd_chunks(s, len);
     if (c > 0) {
-      const int x = x_own + h * c;
+      const int x = x_own + h * (c + s.lead) + s.lead;
       const int c0 = pd_worker_of(x, W, P), c1 = pd_worker_of(x + c - 1, W, P);
       m.no = c1 - c0 + 1;
       const int64_t row = (static_cast<int64_t>(c0) + u) * s.G + g;
@@ -370,19 +372,26 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
     float* acc = p.acc + static_cast<int64_t>(u) * s.T;
     const float* lg = p.logits + static_cast<int64_t>(u) * s.G * p.Tl;
     const int64_t k1 = min(k0 + share, static_cast<int64_t>(len));
-    // four keys a thread: the logits' rows start on 16 bytes, the sums' need not
+    // four keys a thread, four heads' logits in flight: their rows start on 16
+    // bytes, the sums' need not
     for (int64_t j = k0 + 4 * tid; j < k1; j += 4 * kMergeThreads) {
       float w[4] = {0.f, 0.f, 0.f, 0.f}, old[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) old[i] = p.decay != 0.f && j + i < k1 ? acc[j + i] : 0.f;
-      for (int g = 0; g < s.G; ++g) {
-        const float L = lse2[g];
-        const float4 x = ld4(lg + g * p.Tl + j);
-        if (L != -INFINITY) {
-          w[0] += fast_exp2(x.x - L);
-          w[1] += fast_exp2(x.y - L);
-          w[2] += fast_exp2(x.z - L);
-          w[3] += fast_exp2(x.w - L);
+      for (int g0 = 0; g0 < s.G; g0 += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (g0 + g < s.G) x[g] = ld4(lg + (g0 + g) * p.Tl + j);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float L = g0 + g < s.G ? lse2[g0 + g] : -INFINITY;
+          if (L != -INFINITY) {
+            w[0] += fast_exp2(x[g].x - L);
+            w[1] += fast_exp2(x[g].y - L);
+            w[2] += fast_exp2(x[g].z - L);
+            w[3] += fast_exp2(x[g].w - L);
+          }
         }
       }
 #pragma unroll
@@ -440,11 +449,13 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
     a.R = pd_tc_rows(G);
     a.ctas = N > 0 && Tp > 0 && rows > pd_few_rows(G) ? num_sms : 0;
     a.workers = 1;
-    // a chunk's time in 16-key steps of the warps: its bytes, and half as much
-    // again where both halves' rows are at work (groups taken as of equal size)
-    a.cost = 4.f * (N > 0 && rows / N > a.R / 2 ? 1.5f : 1.f);
+    // a chunk's time in 16-key steps of the warps: its bytes, and a quarter more for
+    // the longer way to its first and from its last chunk, or twice its bytes where
+    // both halves' rows are at work (groups taken as of equal size)
+    a.cost = 4.f * (N > 0 && rows / N > a.R / 2 ? 2.f : 1.25f);
     b.cost = 1.f;
     a.chunk_log2 = kPdTcChunkLog2;
+    a.lead = kPdTcLead;
     a.min_rows = pd_few_rows(G) + 1;
     a.max_rows = 1 << 30;
     p->a.halves = 2;
@@ -453,6 +464,7 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
     b.ctas = num_sms;
     b.workers = kPdWarps;
     b.chunk_log2 = kPdWarpChunkLog2;
+    b.lead = kPdWarpLead;
     b.max_rows = b.R;
     p->b.slot_rows = b.R;
   } else {
@@ -460,6 +472,7 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
     b.ctas = kF32Ctas * num_sms;
     b.workers = 1;
     b.chunk_log2 = kF32ChunkLog2;
+    b.lead = kF32Lead;
     b.max_rows = 1 << 30;
     p->b.slot_rows = kF32Rows;
   }
@@ -490,7 +503,6 @@ cudaError_t launch_attend_f32(const Launch& l, const PdParams& p) {
 
 template <int D>
 cudaError_t launch_pd_merge(const Launch& l, const PdParams& p) {
-  cudaLaunchConfig_t cfg = {};
   const PdShape& s = p.b.s;
   const int64_t U = static_cast<int64_t>(s.B) * s.Hkv;
   // about four CTAs per SM: of at least kMergeMinKeys keys where there are
@@ -501,15 +513,8 @@ cudaError_t launch_pd_merge(const Launch& l, const PdParams& p) {
       1, std::min<int64_t>(std::max(by_keys, by_cols), 4ll * l.num_sms / U));
   int64_t share = (s.T + blocks - 1) / blocks;
   share = std::max<int64_t>(4, (share + 3) / 4 * 4);
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(U));
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = l.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p, static_cast<int>(share));
+  return launch_behind(merge_kernel<D>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(U)),
+                       dim3(kMergeThreads), 0, l.stream, p, static_cast<int>(share));
 }
 
 }  // namespace

@@ -49,6 +49,10 @@ constexpr int kPdTcSlotRows = 256;
 constexpr int kPdTcChunkLog2 = 6;
 constexpr int kPdWarps = 8;  // warps of a CTA on line b
 constexpr int kPdWarpChunkLog2 = 4;
+// What a unit costs besides its keys, in chunks' time: its queries, the first
+// chunk's way and its partials.  (Without, the warps that got many units of a
+// few keys were the last by 8 of 30 us.)
+constexpr int kPdTcLead = 2, kPdWarpLead = 2;
 cudaError_t launch_attend_bf16(const Launch& l, const PdParams& p, int D, std::string* why);
 
 }  // namespace csa

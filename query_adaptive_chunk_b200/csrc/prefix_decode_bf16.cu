@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                        const __grid_constant__ CUtensorMap tmQs,
                        const __grid_constant__ CUtensorMap tmO, const TcMaps mp,
                        const PdParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_next();  // the merge
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));

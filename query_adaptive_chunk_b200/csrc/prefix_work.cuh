@@ -9,14 +9,14 @@
 // lines run side by side in one launch, each on the share of the CTAs (one per
 // SM) that its keys are of all (as two launches, the second's CTAs wait for SMs
 // at both ends: 42 against 32 us for 32 sequences over 8K tokens).  A unit's
-// keys are cut into chunks.  All chunks of a line's units lie end to end
-// (prefixes first; within a prefix by head, then row tile; own units by
-// sequence, then head) and worker c (a CTA, or a warp) of P takes chunks
-// [W c / P, W (c + 1) / P): every SM streams the same number of keys whatever the
-// lengths.  A worker that holds any of unit i's chunks writes one partial
-// (normalised rows and their log2-sum-exp) to slot c + i: the pairs (c, i) met
-// along the line grow by one in c or in i at a time, so slots are distinct
-// and number at most P + units.
+// keys are cut into chunks.  A unit is `lead` places, for what it costs besides
+// its keys, and its chunks; all units of a line lie end to end (prefixes first;
+// within a prefix by head, then row tile; own units by sequence, then head)
+// and worker c (a CTA, or a warp) of P takes places [W c / P, W (c + 1) / P): every
+// worker has the same to do whatever the lengths.  A worker that holds any of
+// unit i's chunks writes one partial (normalised rows and their log2-sum-exp)
+// to slot c + i: the pairs (c, i) met along the line grow by one in c or in i at
+// a time, so slots are distinct and number at most P + units.
 #pragma once
 
 #include "internal.h"
@@ -42,6 +42,7 @@ struct PdShape {
   int ctas;                    // CTAs that the lines share (0: no such line)
   int workers;                 // workers per CTA, at most 8
   int chunk_log2;              // keys per chunk
+  int lead;                    // places before a unit's chunks
   int min_rows, max_rows;      // prefix units of groups of so many rows
   int own;                     // own units too
   float cost;                  // of a chunk, relative to the other line's
@@ -71,6 +72,10 @@ __device__ __forceinline__ int pd_item_keys(const PdShape& s, int i) {
 }
 __device__ __forceinline__ int pd_chunks(const PdShape& s, int keys) {
   return (keys + (1 << s.chunk_log2) - 1) >> s.chunk_log2;
+}
+// Places of a unit of so many keys.
+__device__ __forceinline__ int pd_places(const PdShape& s, int keys) {
+  return keys > 0 ? s.lead + pd_chunks(s, keys) : 0;
 }
 // Row tiles of a group of `seqs` sequences (0: the group is not on this line).
 __device__ __forceinline__ int pd_tiles(const PdShape& s, int seqs) {
@@ -109,7 +114,7 @@ __device__ __forceinline__ void pd_groups(const PdShape& s, int* gs) {
   }
 }
 
-// A worker's place on the line: `left` chunks from chunk `off` of item `item`
+// A worker's stretch of the line: `left` places from place `off` of item `item`
 // on; unit0 prefix units lie before it (prefix items only).
 struct PdStart {
   int left, item, off, unit0;
@@ -117,7 +122,7 @@ struct PdStart {
 
 // What the merge needs to find a unit's partials, written by one CTA.
 struct PdPlan {
-  int32_t* starts;  // [N + B + 2] first chunk of each item, then W, then P
+  int32_t* starts;  // [N + B + 2] first place of each item, then W, then P
   int32_t* ubase;   // [N] first unit of each prefix
   int32_t* gsan;    // [N + 1] the sanitised group bounds (line b's plan)
   int32_t* group;   // [B] each sequence's prefix, or -1 (line b's plan)
@@ -146,7 +151,7 @@ __device__ __forceinline__ uint64_t pd_scan(uint64_t v, uint64_t* sh, uint64_t* 
   return (warp > 0 ? before : 0) + x - v;
 }
 
-// Chunks of W before worker c of P (c <= P <= 2^15).
+// Places of W before worker c of P (c <= P <= 2^15).
 __device__ __forceinline__ int pd_cut(int W, int c, int P) {
   const int q = W / P;
   return q * c + (W - q * P) * c / P;
@@ -170,12 +175,12 @@ __device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b,
   auto units = [&](const PdShape& s, int i) -> int {
     return i < s.N ? pd_tiles(s, gs[i + 1] - gs[i]) * s.Hkv : s.own ? s.Hkv : 0;
   };
-  // chunks of item i: line a in the high half, line b in the low one
+  // places of item i: line a in the high half, line b in the low one
   auto weigh = [&](int i, int raw) -> uint64_t {
     if (i >= items) return 0;
     const int keys = pd_clamp(raw, i < b.N ? b.Tp : b.T, b.err);
-    const uint32_t nb = units(b, i) * pd_chunks(b, keys);
-    const uint32_t na = two && i < b.N ? units(a, i) * pd_chunks(a, keys) : 0;
+    const uint32_t nb = units(b, i) * pd_places(b, keys);
+    const uint32_t na = two && i < b.N ? units(a, i) * pd_places(a, keys) : 0;
     return static_cast<uint64_t>(na) << 32 | nb;
   };
   auto raw_of = [&](int i) { return i < items ? pd_raw_keys(b, i) : 0; };
@@ -199,9 +204,16 @@ __device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b,
   int na = 0;
   if (Wa > 0) {
     const float ca = Wa * a.cost, cb = Wb * b.cost;
-    na = Wb == 0 ? b.ctas : max(1, min(b.ctas - 1, __float2int_rn(b.ctas * ca / (ca + cb))));
+    const int most = Wb == 0 ? b.ctas : b.ctas - 1;
+    na = Wb == 0 ? most : max(1, min(most, __float2int_rn(b.ctas * ca / (ca + cb))));
+    // units of one length: a whole number of CTAs each, so that none works on two
+    const int u = b.N == 1 ? units(a, 0) : 0;
+    if (u > 0 && na >= u) {
+      na = (na + u / 2) / u * u;
+      if (na > most) na -= u;
+    }
   }
-  // each worker that takes part has a chunk
+  // each worker that takes part has a place
   const int Pa = max(1, min(na, Wa)), Pb = max(1, min((b.ctas - na) * b.workers, Wb));
   const bool on_a = static_cast<int>(blockIdx.x) < na;
   const PdShape& me = on_a ? a : b;
@@ -214,7 +226,7 @@ __device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b,
 #pragma unroll 1
     for (int k = 0; k < nw; ++k) {
       const int x0 = __shfl_sync(0xffffffffu, x_lane, k), x1 = __shfl_sync(0xffffffffu, x_lane, k + 1);
-      if (x1 > x0 && x0 >= e && x0 < e + n) {  // chunks [e, e + n) are item i's
+      if (x1 > x0 && x0 >= e && x0 < e + n) {  // places [e, e + n) are item i's
         st[k].left = x1 - x0;
         st[k].item = i;
         st[k].off = x0 - e;
@@ -289,61 +301,65 @@ struct PdSeg {
 struct PdWalk {
   const PdShape& s;
   const int* gs;
-  int left, item, h = 0, tile = 0, j = 0, unit0;
-  int off;                  // chunks of `item` before the start
+  int left, item, h = 0, tile = 0, j = 0, unit0;  // j: place in the unit
+  int off;                  // places of `item` before the start
   int keys = 0, tiles = 0;  // of `item`, once loaded
   bool loaded = false;
   __device__ __forceinline__ PdWalk(const PdShape& sh, const int* g, const PdStart& st)
       : s(sh), gs(g), left(st.left), item(st.item), unit0(st.unit0), off(st.off) {}
   __device__ __forceinline__ bool next(PdSeg& q) {
-    if (left <= 0) return false;
-    while (!loaded) {
-      if (item >= s.N + s.B) return false;
-      keys = pd_item_keys(s, item);
-      tiles = item < s.N ? pd_tiles(s, gs[item + 1] - gs[item]) : s.own;
-      loaded = keys > 0 && tiles > 0;
+    while (left > 0) {
       if (!loaded) {
-        unit0 += tiles * s.Hkv;  // only read for prefixes
-        ++item;
-      }
-    }
-    const int c = pd_chunks(s, keys);
-    if (off > 0) {  // the first segment of all
-      const int ui = off / c;
-      h = ui / tiles;
-      tile = ui - h * tiles;
-      j = off - ui * c;
-      off = 0;
-    }
-    q.own = item >= s.N;
-    q.n = q.own ? 0 : item;
-    q.b = q.own ? item - s.N : 0;
-    q.h = h;
-    q.keys = keys;
-    q.unit = q.own ? q.b * s.Hkv + h : unit0 + h * tiles + tile;
-    q.row0 = (q.own ? q.b : gs[item]) * s.G + tile * s.R;
-    q.rows = q.own ? s.G : min(s.R, (gs[item + 1] - gs[item]) * s.G - tile * s.R);
-    q.j0 = j;
-    q.j1 = min(c, j + left);
-    left -= q.j1 - j;
-    j = q.j1;
-    if (j == c) {
-      j = 0;
-      if (++tile == tiles) {
-        tile = 0;
-        if (++h == s.Hkv) {
-          h = 0;
-          unit0 += tiles * s.Hkv;
+        if (item >= s.N + s.B) return false;
+        keys = pd_item_keys(s, item);
+        tiles = item < s.N ? pd_tiles(s, gs[item + 1] - gs[item]) : s.own;
+        loaded = keys > 0 && tiles > 0;
+        if (!loaded) {
+          unit0 += tiles * s.Hkv;  // only read for prefixes
           ++item;
-          loaded = false;
+          continue;
         }
       }
+      const int c = pd_places(s, keys);
+      if (off > 0) {  // the first segment of all
+        const int ui = off / c;
+        h = ui / tiles;
+        tile = ui - h * tiles;
+        j = off - ui * c;
+        off = 0;
+      }
+      q.own = item >= s.N;
+      q.n = q.own ? 0 : item;
+      q.b = q.own ? item - s.N : 0;
+      q.h = h;
+      q.keys = keys;
+      q.unit = q.own ? q.b * s.Hkv + h : unit0 + h * tiles + tile;
+      q.row0 = (q.own ? q.b : gs[item]) * s.G + tile * s.R;
+      q.rows = q.own ? s.G : min(s.R, (gs[item + 1] - gs[item]) * s.G - tile * s.R);
+      const int to = min(c, j + left);
+      q.j0 = max(0, j - s.lead);
+      q.j1 = max(0, to - s.lead);
+      left -= to - j;
+      j = to;
+      if (j == c) {
+        j = 0;
+        if (++tile == tiles) {
+          tile = 0;
+          if (++h == s.Hkv) {
+            h = 0;
+            unit0 += tiles * s.Hkv;
+            ++item;
+            loaded = false;
+          }
+        }
+      }
+      if (q.j1 > q.j0) return true;  // (a stretch that ends in a unit's lead has none of it)
     }
-    return true;
+    return false;
   }
 };
 
-// The worker of P that holds chunk x of W: (x + 1) P - 1 < 2^46 is exact in
+// The worker of P that holds place x of W: (x + 1) P - 1 < 2^46 is exact in
 // 64-bit floats, and the quotient is at least 2^-31 away from the next integer.
 __device__ __forceinline__ int pd_worker_of(int x, int W, int P) {
   return static_cast<int>((static_cast<double>(x + 1) * P - 1.0) / W);
