@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -422,6 +423,11 @@ class RotaryDesc(ctypes.Structure):
     ]
 
 
+# The same layout packed in one call: a RotaryDesc takes 5 us to fill, as long as
+# the launch.
+ROTARY_PACK = struct.Struct("@PPi6qPPi6qiiqiiiiPfPqq")
+
+
 class CacheDesc(ctypes.Structure):
     """ctypes mirror of csa_cache_desc."""
     _fields_ = [
@@ -489,8 +495,9 @@ def csa_rotary_table(rot, theta, scaling, factor, orig_len, low, high, freqs, ta
                                 _p(table), _s(stream)))
 
 
-def csa_rotary(desc: RotaryDesc, stream=None):
-    _check(lib.csa_rotary(ctypes.byref(desc), _s(stream)))
+def csa_rotary(desc, stream=None):
+    """desc: a RotaryDesc, or its fields packed by ROTARY_PACK."""
+    _check(lib.csa_rotary(desc if type(desc) is bytes else ctypes.byref(desc), _s(stream)))
 
 
 def csa_cache_insert(desc: CacheDesc, k, k_stride, v, v_stride, stream=None):

@@ -359,7 +359,7 @@ class Rotary:
             q_out = torch.empty_like(q)
         x = (q.data_ptr(), q_out.data_ptr(), Hq, _rows("q", q, dt),
              _rows("q_out", q_out, dt, q.shape))
-        x2 = (None, None, 0, (0, 0, 0), (0, 0, 0))
+        x2 = (0, 0, 0, (0, 0, 0), (0, 0, 0))
         if k is not None:
             if k_out is None:
                 k_out = torch.empty_like(k)
@@ -368,7 +368,7 @@ class Rotary:
                   _rows("k_out", k_out, dt, k.shape))
             if k.device != dev or k_out.device != dev:
                 _bad(f"k and k_out must be on {dev}")
-        pos = stride = None
+        pos = stride = 0
         if positions is not None:
             if positions.dtype != torch.int32 or positions.shape != (B, S) or positions.device != dev:
                 _bad(f"positions must be int32 of shape {(B, S)} on {dev}")
@@ -378,8 +378,9 @@ class Rotary:
             pos = positions.data_ptr()
         if q.device != dev or q_out.device != dev:
             _bad(f"q and q_out must be on {dev}")
-        csa.csa_rotary(csa.RotaryDesc(*x, *x2, csa._dt(dt), B, S, D, self.rot, self.layout, transpose,
-                                      self.table_ptr, self.amplitude, pos, stride or 0, pos0), stream)
+        csa.csa_rotary(csa.ROTARY_PACK.pack(
+            x[0], x[1], x[2], *x[3], *x[4], x2[0], x2[1], x2[2], *x2[3], *x2[4], csa._dt(dt), B, S, D,
+            self.rot, self.layout, transpose, self.table_ptr, self.amplitude, pos, stride, pos0), stream)
         return q_out if k is None else (q_out, k_out)
 
 

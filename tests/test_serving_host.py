@@ -118,6 +118,17 @@ def test_descriptor_layouts(csa, py, c):
     assert vals[1:] == [getattr(cls, f).offset for f in fields]
 
 
+def test_rotary_pack_is_the_descriptor(csa):
+    d = csa.RotaryDesc(1, 2, 3, (4, 5, 6), (7, 8, 9), 10, 11, 12, (13, 14, 15), (16, 17, 18), 1, 20, 21, 22, 23, 1, 1,
+                       24, 2.5, 25, 26, -27)
+    flat = csa.ROTARY_PACK.pack(1, 2, 3, *range(4, 10), 10, 11, 12, *range(13, 19), 1, 20, 21, 22, 23, 1, True, 24, 2.5,
+                                25, 26, -27)
+    e = csa.RotaryDesc.from_buffer_copy(flat)
+    for f, _ in d._fields_:
+        a, b = getattr(d, f), getattr(e, f)
+        assert (list(a) == list(b)) if isinstance(a, ctypes.Array) else a == b, f
+
+
 INVALID, UNSUPPORTED = 1, 2
 
 
