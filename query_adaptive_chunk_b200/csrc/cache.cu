@@ -145,12 +145,10 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
 // distributed shared memory; keys equal to tau are taken lowest row first.
 // Each CTA writes its kept rows, ascending, into the destination's positions
 // (as row numbers; the copy turns them into positions).  Each warp takes a run of
-// consecutive keys, a lane per key, so that counts and places come from
-// ballots and shared memory is read without bank conflicts (the histograms by
-// atomics on one copy per warp; a match of equal buckets first took four
-// times as long).  The weights are
-// read once, eight a thread in flight; bound by the passes' latency (4 with two
-// cluster barriers each).
+// consecutive keys, four a lane (histograms by atomics on one copy per warp; a
+// match of equal buckets first took four times as long).  The weights are read
+// once, sixteen a thread in flight; bound by the passes' latency (four, one
+// cluster barrier each).
 constexpr int kCmpThreads = 512;
 constexpr int kCmpKeys = 49152;  // keys held per CTA (192 KB)
 
@@ -177,27 +175,35 @@ __device__ __forceinline__ int source_len(const int32_t* len, int b, int64_t S, 
   return n;
 }
 
+// Four consecutive keys from j on (j a multiple of four); 0, which no key is, for
+// those at or past n.
+struct Keys4 {
+  uint32_t k[4];
+};
+
 template <int CS>
 __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const CompressParams p) {
   if (CS > 1) cluster_arrive_relaxed();
   pdl_next();  // the copy
+  constexpr int kWarps = kCmpThreads / 32;
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ unsigned int hw[kCmpThreads / 32][256];  // a histogram per warp: no contention between them
-  __shared__ unsigned int hc[256], gc[256];
-  __shared__ unsigned int part_eq[CS], part_sel[CS];
-  __shared__ int scan_sh[33];
+  __shared__ unsigned int hw[kWarps][256];  // a histogram per warp: no contention between them
+  __shared__ unsigned int hc[2][256];       // this CTA's, for the pass's parity
+  __shared__ unsigned int gc[256];          // the cluster's
+  __shared__ unsigned int part[2][CS];      // keys above tau and at tau of each CTA
+  __shared__ unsigned int warp_part[2][kWarps];
   __shared__ unsigned int pick_sh[2];
   const int rank = CS > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int u = blockIdx.x / CS, b = u / p.Hkv, tid = threadIdx.x, lane = tid & 31;
+  const int warp = tid >> 5;
   const int len = source_len(p.len, b, p.S, p.err);
   const int next = p.next_pos ? p.next_pos[b] : len;
   const int lo = static_cast<int>(static_cast<int64_t>(len) * rank / CS);
   const int n = static_cast<int>(static_cast<int64_t>(len) * (rank + 1) / CS) - lo;
   const float* wrow = p.weights + static_cast<int64_t>(u) * p.S + lo;
   const int32_t* prow = p.positions ? p.positions + static_cast<int64_t>(u) * p.S + lo : nullptr;
-  auto make_key = [&](int j) -> uint32_t {
-    const int pos = prow ? prow[j] : lo + j;
-    return is_protected(pos, next, p.n_sink, p.n_local) ? kKeyProtected : weight_key(wrow[j]);
+  auto make_key = [&](float w, int pos) -> uint32_t {
+    return is_protected(pos, next, p.n_sink, p.n_local) ? kKeyProtected : weight_key(w);
   };
   const bool select = len > p.budget;
   int32_t* out = p.rows + static_cast<int64_t>(u) * p.T;
@@ -208,69 +214,94 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
   }
   const bool held = p.held != 0;
   if (held) {
-    constexpr int U = 8;  // loads in flight
+    constexpr int U = 16;  // loads in flight
     for (int j0 = tid; j0 < n; j0 += U * kCmpThreads) {
       float w[U];
-      int pos[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int j = j0 + i * kCmpThreads;
         w[i] = j < n ? wrow[j] : 0.f;
-        pos[i] = prow && j < n ? prow[j] : lo + j;
       }
+      if (prow == nullptr) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int j = j0 + i * kCmpThreads;
-        if (j < n)
-          keys[j] = is_protected(pos[i], next, p.n_sink, p.n_local) ? kKeyProtected : weight_key(w[i]);
+        for (int i = 0; i < U; ++i) {
+          const int j = j0 + i * kCmpThreads;
+          if (j < n) keys[j] = make_key(w[i], lo + j);
+        }
+      } else {
+        int pos[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int j = j0 + i * kCmpThreads;
+          pos[i] = j < n ? prow[j] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int j = j0 + i * kCmpThreads;
+          if (j < n) keys[j] = make_key(w[i], pos[i]);
+        }
       }
     }
   }
-  auto key_at = [&](int j) -> uint32_t { return held ? keys[j] : make_key(j); };
   __syncthreads();
-  // this warp's run of the CTA's rows
-  constexpr int kWarps = kCmpThreads / 32;
-  const int warp = tid >> 5;
-  const int run = (n + kWarps * 32 - 1) / (kWarps * 32) * 32;
+  auto keys_at = [&](int j) -> Keys4 {
+    Keys4 k;
+    if (held) {
+      const uint4 x = *reinterpret_cast<const uint4*>(keys + j);  // (the buffer is whole fours)
+      k.k[0] = x.x;
+      k.k[1] = x.y;
+      k.k[2] = x.z;
+      k.k[3] = x.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        k.k[i] = j + i < n ? make_key(wrow[j + i], prow ? prow[j + i] : lo + j + i) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (j + i >= n) k.k[i] = 0u;
+    return k;
+  };
+  // this warp's run of the CTA's rows, a multiple of 128 rows from its start
+  const int run = (n + kWarps * 128 - 1) / (kWarps * 128) * 128;
   const int s0 = min(n, warp * run), s1 = min(n, s0 + run);
   // keys > tau are taken, and the first `need` keys equal to tau
   uint32_t prefix = 0u, mask = 0u;
   unsigned int need = static_cast<unsigned int>(p.budget);
   for (int shift = 24; shift >= 0; shift -= 8) {
+    unsigned int* mine = hc[(shift >> 3) & 1];
     for (int d = lane; d < 256; d += 32) hw[warp][d] = 0u;
     __syncwarp();
-    for (int j0 = s0; j0 < s1; j0 += 32) {
-      const int j = j0 + lane;
-      if (j < s1) {
-        const uint32_t key = key_at(j);
-        if ((key & mask) == prefix) atomicAdd(&hw[warp][(key >> shift) & 255u], 1u);
-      }
+    for (int j = s0 + 4 * lane; j < s1; j += 128) {
+      const Keys4 k = keys_at(j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k.k[i] != 0u && (k.k[i] & mask) == prefix) atomicAdd(&hw[warp][(k.k[i] >> shift) & 255u], 1u);
     }
     __syncthreads();
     if (tid < 256) {
       unsigned int sum = 0u;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) sum += hw[w][tid];
-      hc[tid] = sum;
+      mine[tid] = sum;
+      if (CS == 1) gc[tid] = sum;
     }
     if (CS > 1) {
-      cluster_arrive();  // every CTA's histogram of this pass is complete
+      // every CTA's histogram of this pass is complete.  The buffer is written
+      // again two passes on, behind the next pass's barrier: by then all have
+      // read it.
+      cluster_arrive();
       cluster_wait();
-      for (int d = tid; d < 256; d += kCmpThreads) {
+      if (tid < 256) {
         unsigned int cr[CS], cnt = 0u;
 #pragma unroll
-        for (int r = 0; r < CS; ++r) cr[r] = ld_cluster_u32(cluster_map(smem_u32(hc + d), r));
+        for (int r = 0; r < CS; ++r) cr[r] = ld_cluster_u32(cluster_map(smem_u32(mine + tid), r));
 #pragma unroll
         for (int r = 0; r < CS; ++r) cnt += cr[r];
-        gc[d] = cnt;
+        gc[tid] = cnt;
       }
-      cluster_arrive();  // every CTA has read the others' histograms (they may be cleared)
-      cluster_wait();
-    } else {
-      __syncthreads();
-      for (int d = tid; d < 256; d += kCmpThreads) gc[d] = hc[d];
-      __syncthreads();
     }
+    __syncthreads();
     if (tid < 32) {  // the bucket where the count from the top reaches `need`
       unsigned int pc[8], lc = 0u;
 #pragma unroll
@@ -309,53 +340,77 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
     prefix |= pick_sh[0] << shift;
     mask |= 255u << shift;
     need -= pick_sh[1];
-    __syncthreads();  // pick_sh read before the next pass writes it
   }
   const uint32_t tau = prefix;
-  // of this warp's run: keys above tau, keys at tau
-  int c_gt = 0, c_eq = 0;
-  for (int j0 = s0; j0 < s1; j0 += 32) {
-    const bool in = j0 + lane < s1;
-    const uint32_t key = in ? key_at(j0 + lane) : 0u;
-    c_gt += __popc(__ballot_sync(0xffffffffu, in && key > tau));
-    c_eq += __popc(__ballot_sync(0xffffffffu, in && key == tau));
+  // keys above tau and at tau: of each warp, then of each CTA
+  unsigned int c_gt = 0, c_eq = 0;
+  for (int j = s0 + 4 * lane; j < s1; j += 128) {
+    const Keys4 k = keys_at(j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c_gt += k.k[i] > tau;
+      c_eq += k.k[i] == tau && k.k[i] != 0u;
+    }
   }
-  // lane 0 speaks for its warp in the block's sums
-  int eq_tot = 0, eq_before = 0;
-  const int eq_base = __shfl_sync(
-      0xffffffffu, block_exclusive_scan(lane == 0 ? c_eq : 0, scan_sh, &eq_tot), 0);
-  if (CS > 1) {
-    if (tid < CS)
-      st_cluster_u32(cluster_map(smem_u32(part_eq + rank), tid), static_cast<unsigned int>(eq_tot));
-    cluster_arrive();
-    cluster_wait();
-    for (int r = 0; r < rank; ++r) eq_before += static_cast<int>(part_eq[r]);
+  c_gt = __reduce_add_sync(0xffffffffu, c_gt);
+  c_eq = __reduce_add_sync(0xffffffffu, c_eq);
+  if (lane == 0) {
+    warp_part[0][warp] = c_gt;
+    warp_part[1][warp] = c_eq;
   }
-  const int take = max(0, min(static_cast<int>(need) - eq_before, eq_tot));  // ties kept here
-  const int c_sel = c_gt + max(0, min(take - eq_base, c_eq));
-  int sel_tot = 0, sel_before = 0;
-  const int sel_base = __shfl_sync(
-      0xffffffffu, block_exclusive_scan(lane == 0 ? c_sel : 0, scan_sh, &sel_tot), 0);
+  __syncthreads();
+  unsigned int gt = 0, eq = 0;  // before this warp
+  for (int w = 0; w < warp; ++w) {
+    gt += warp_part[0][w];
+    eq += warp_part[1][w];
+  }
   if (CS > 1) {
-    if (tid < CS)
-      st_cluster_u32(cluster_map(smem_u32(part_sel + rank), tid),
-                     static_cast<unsigned int>(sel_tot));
+    if (tid < CS) {
+      unsigned int a0 = 0, a1 = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        a0 += warp_part[0][w];
+        a1 += warp_part[1][w];
+      }
+      st_cluster_u32(cluster_map(smem_u32(&part[0][rank]), tid), a0);
+      st_cluster_u32(cluster_map(smem_u32(&part[1][rank]), tid), a1);
+    }
     cluster_arrive();
     cluster_wait();  // the last access to another CTA's shared memory is before this barrier
-    for (int r = 0; r < rank; ++r) sel_before += static_cast<int>(part_sel[r]);
+    for (int r = 0; r < rank; ++r) {
+      gt += part[0][r];
+      eq += part[1][r];
+    }
   }
-  int at = sel_before + sel_base, eq_seen = eq_base;
-  const unsigned int below = (1u << lane) - 1u;
-  for (int j0 = s0; j0 < s1; j0 += 32) {
-    const bool in = j0 + lane < s1;
-    const uint32_t key = in ? key_at(j0 + lane) : 0u;
-    const unsigned int eq = __ballot_sync(0xffffffffu, in && key == tau);
-    const bool t = in && (key > tau || (key == tau && eq_seen + __popc(eq & below) < take));
-    const unsigned int sel = __ballot_sync(0xffffffffu, t);
-    const int to = at + __popc(sel & below);
-    if (t && to < p.budget) out[to] = lo + j0 + lane;
-    at += __popc(sel);
-    eq_seen += __popc(eq);
+  // Row j goes behind the keys above tau and the kept ties before it.  A lane
+  // has four rows; those of the lanes below come from a scan of the counts.
+  for (int j0 = s0; j0 < s1; j0 += 128) {
+    const int j = j0 + 4 * lane;
+    Keys4 k{};
+    if (j < s1) k = keys_at(j);
+    unsigned int mine = 0;  // above tau in the low half, at tau in the high one
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      mine += (k.k[i] > tau ? 1u : 0u) + (k.k[i] == tau && k.k[i] != 0u ? 65536u : 0u);
+    unsigned int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const unsigned int all = __shfl_sync(0xffffffffu, sum, 31);
+    unsigned int g = gt + ((sum - mine) & 0xffffu), q = eq + ((sum - mine) >> 16);
+    if (mine != 0u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool above = k.k[i] > tau, tie = k.k[i] == tau && k.k[i] != 0u;
+        const unsigned int to = g + min(q, need);
+        if ((above || (tie && q < need)) && to < static_cast<unsigned int>(p.budget)) out[to] = lo + j + i;
+        g += above;
+        q += tie;
+      }
+    }
+    gt += all & 0xffffu;
+    eq += all >> 16;
   }
 }
 
@@ -484,7 +539,7 @@ cudaError_t launch_cache_compress(const Launch& l, const CacheArgs& dst, const C
     while (CS < 8 && (s.S + CS - 1) / CS > kCmpKeys) CS *= 2;
     const int64_t per = (s.S + CS - 1) / CS;
     p.held = per <= kCmpKeys ? 1 : 0;
-    const size_t smem = p.held ? static_cast<size_t>(per) * 4 : 0;
+    const size_t smem = p.held ? static_cast<size_t>(per + 3) / 4 * 16 : 0;  // fours of keys
     const cudaError_t e = CS == 1   ? launch_compress_select<1>(l, p, U, smem)
                           : CS == 2 ? launch_compress_select<2>(l, p, U, smem)
                           : CS == 4 ? launch_compress_select<4>(l, p, U, smem)
