@@ -624,7 +624,7 @@ CSA_API csa_status csa_block_sparse_prefill(const void* Q, const void* K, const 
  *                      lo, 0.001), 0, 1), lo = max(0, floor(d(high))), hi =
  *                      min(rot - 1, ceil(d(low))), d(t) = rot ln(orig_len /
  *                      (2 pi t)) / (2 ln theta): the ramp over the pair index
- * `freqs` (device, rot/2 doubles, radians per position) replaces the formula
+ * `freqs` (device, rot/2 finite doubles, radians per position) replaces the formula
  * when not NULL; the other numbers are then not used.
  *   rot even, 2 <= rot <= 512;  theta > 1;  factor >= 1;  orig_len >= 1 and
  *   0 < low < high where they are used.  table: rot/2 uint64 (output). */
@@ -739,7 +739,8 @@ CSA_API csa_status csa_cache_insert(const csa_cache_desc* c, const void* k,
  *   src K, V by strides (sequence, head, row); weights [B, Hkv, S] fp32;
  *   positions NULL (the row number) or [B, Hkv, S] int32; src_next_pos NULL
  *   (n) or [B], required with positions.  n_sink + n_local <= budget.
- *   Source and cache must not overlap.  S < 2^31; c->counters is not used. */
+ *   Source and cache (len among them) must not overlap.  S < 2^31; c->counters is
+ *   not used. */
 typedef struct csa_cache_source {
   const void* K;
   const void* V;
@@ -776,8 +777,9 @@ CSA_API csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_s
  *   len NULL (T) or [B] int32
  *   CSA_BF16: bf16 tensor-core products, weights of V rounded to bf16, fp32
  *   sums and statistics; CSA_F32: fp32 throughout.  D in {64, 128};  G <= 16;
- *   N <= 64;  strides multiples of 16 bytes;  B * Hkv <= 65535.
- * A length or group bound out of range records CSA_ERR_DEVICE_INDEX and is clamped.
+ *   N <= 64;  strides multiples of 16 bytes, the tokens' at least D;  B * Hkv <= 65535.
+ * A length or group bound out of range records CSA_ERR_DEVICE_INDEX and is
+ * clamped.  Lengths and bounds must not change while the call runs.
  *   workspace >= csa_prefix_decode_workspace_bytes(...) (current device), not
  *   kept between calls and needing no initial value; calls that share one
  *   must not overlap on the GPU. */

@@ -1303,7 +1303,9 @@ csa_status prefix_sizes(csa_dtype dtype, int B, int Hq, int Hkv, int D, int N, i
   return CSA_OK;
 }
 
-csa_status strides16(const int64_t* st, int es, const char* name) {
+csa_status strides16(const int64_t* st, int es, int64_t rows, int D, const char* name) {
+  CSA_SUPPORT(rows <= 1 || st[2] < 0 || st[2] >= D,
+              std::string(name) + ": strides of the tokens must be at least D");
   for (int i = 0; i < 3; ++i) {
     CSA_REQUIRE(st[i] >= 0, std::string(name) + ": strides must be non-negative");
     CSA_SUPPORT(st[i] * es % 16 == 0, std::string(name) + ": strides must be multiples of 16 bytes");
@@ -1406,7 +1408,14 @@ csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* s
   CSA_SUPPORT(s->S < 2147483648LL, "S must be < 2^31");
   CSA_REQUIRE(s->positions == nullptr || s->next_pos != nullptr,
               "source positions need the source's next_pos");
-  CSA_REQUIRE(s->len == nullptr || s->len != c->len, "the source's len must not be the cache's");
+  if (s->len != nullptr) {
+    Extent x, y;
+    x.lo = reinterpret_cast<uintptr_t>(s->len);
+    x.hi = x.lo + static_cast<uintptr_t>(c->B) * 4;
+    y.lo = reinterpret_cast<uintptr_t>(c->len);
+    y.hi = y.lo + static_cast<uintptr_t>(c->B) * 4;
+    CSA_REQUIRE(!x.overlaps(y), "the source's len must not be the cache's");
+  }
   if (c->B == 0) return CSA_OK;
   Extent ek, ev, sk, sv;
   CSA_TRY(cache_ptrs(c, false, &ek, &ev));
@@ -1475,14 +1484,14 @@ csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream)
   if (d->B == 0) return CSA_OK;
   const int es = dtype_size(d->dtype);
   if (d->N > 0 && d->Tp > 0) {
-    CSA_TRY(strides16(d->kp_stride, es, "Kp"));
-    CSA_TRY(strides16(d->vp_stride, es, "Vp"));
+    CSA_TRY(strides16(d->kp_stride, es, d->Tp, d->D, "Kp"));
+    CSA_TRY(strides16(d->vp_stride, es, d->Tp, d->D, "Vp"));
     CSA_TRY(check_ptr(d->Kp, "Kp"));
     CSA_TRY(check_ptr(d->Vp, "Vp"));
   }
   if (d->T > 0) {
-    CSA_TRY(strides16(d->k_stride, es, "K"));
-    CSA_TRY(strides16(d->v_stride, es, "V"));
+    CSA_TRY(strides16(d->k_stride, es, d->T, d->D, "K"));
+    CSA_TRY(strides16(d->v_stride, es, d->T, d->D, "V"));
     CSA_TRY(check_ptr(d->K, "K"));
     CSA_TRY(check_ptr(d->V, "V"));
   }

@@ -327,6 +327,7 @@ struct PdWalk {
         tile = ui - h * tiles;
         j = off - ui * c;
         off = 0;
+        if (h >= s.Hkv) return false;  // the lengths have changed since: nothing past the heads
       }
       q.own = item >= s.N;
       q.n = q.own ? 0 : item;

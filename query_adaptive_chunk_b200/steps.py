@@ -295,6 +295,25 @@ def _bad(why: str):
     raise csa.CsaError(1, why)
 
 
+_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _typed(name, dtype):
+    if dtype not in _TYPES:
+        _bad(f"{name} must be bf16 or fp32, not {dtype}")
+
+
+def _empty_like(t, stream):
+    """An output for a call on `stream`: allocated on it, so that its memory is
+    not one that other streams' pending work still uses."""
+    if stream is None:
+        return torch.empty_like(t)
+    if not isinstance(stream, torch.cuda.Stream):
+        _bad("give the outputs with a raw stream")
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _same_device(device, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != device:
@@ -350,19 +369,22 @@ class Rotary:
         """Turns q [B, S, Hq, D] and k [B, S, Hkv, D] (any strides, the last
         index dense; a decode step has S = 1) in one launch.  positions: int32
         [B, S] (rows may repeat: expand a [1, S]), else pos0 + s.  Results go to
-        q_out / k_out (q_out=q: in place), new tensors by default.
+        q_out / k_out (q_out=q: in place), by default new tensors of `stream`
+        (then a torch stream).
         transpose=True gives the gradient of the input from that of the output.
         Returns (q_out, k_out), or q_out alone without k."""
         B, S, Hq, D = q.shape
         dt, dev = q.dtype, self.table.device
+        if dt not in _TYPES:
+            _typed("q", dt)
         if q_out is None:
-            q_out = torch.empty_like(q)
+            q_out = _empty_like(q, stream)
         x = (q.data_ptr(), q_out.data_ptr(), Hq, _rows("q", q, dt),
              _rows("q_out", q_out, dt, q.shape))
         x2 = (0, 0, 0, (0, 0, 0), (0, 0, 0))
         if k is not None:
             if k_out is None:
-                k_out = torch.empty_like(k)
+                k_out = _empty_like(k, stream)
             Hkv = k.shape[2]
             x2 = (k.data_ptr(), k_out.data_ptr(), Hkv, _rows("k", k, dt, (B, S, Hkv, D)),
                   _rows("k_out", k_out, dt, k.shape))
@@ -402,6 +424,7 @@ class TokenCache:
                  n_local: int = 0):
         B, Hkv, T, D = K.shape
         dev = K.device
+        _typed("K", K.dtype)
 
         def own(name, t, dtype, shape):
             return torch.zeros(shape, dtype=dtype, device=dev) if t is None else _dense(name, t, dtype, shape)
@@ -464,6 +487,7 @@ class SharedPrefixDecoder:
                  scale: float | None = None, out_dtype=torch.float32, rotary: Rotary | None = None):
         B, Hkv, T, D, dt, dev = cache.B, cache.Hkv, cache.T, cache.D, cache.K.dtype, cache.K.device
         self.cache, self.Hq, self.rotary = cache, Hq, rotary
+        _typed("out_dtype", out_dtype)
         N = Tp = 0
         kw = {}
         if Kp is not None:

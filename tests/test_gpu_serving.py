@@ -18,6 +18,7 @@ import pytest
 import torch
 
 from oracle import serving as S
+from oracle.serving import rotary_freqs as oracle_freqs
 from oracle.pipeline import to_np
 
 pytestmark = pytest.mark.gpu
@@ -550,3 +551,157 @@ def test_two_streams_with_their_own_workspaces(steps, csa):
     csa.csa_check_device_status()
     for d, (o, l, w) in zip(decs, want):
         assert torch.equal(d.out, o) and torch.equal(d.lse, l) and torch.equal(d.cache.weights, w)
+
+
+# ---------------------------------------------------------------- what no ordinary call has
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [4, 12])
+def test_decode_nan_stays_in_its_rows(steps, csa, dtype, G):
+    """A NaN or infinity in a query or in a valid key makes the rows that see it NaN,
+    the others keep their values."""
+    B, Hkv, D, T, Tp = 20, 2, 64, 150, 200
+    lens = [150] * B
+    q, K, V, Kp, Vp = _decode_case(dtype, B, Hkv, G, D, 1, Tp, T, [Tp], [0, 16], lens, 8, poison=False)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+
+    def run():
+        cache = steps.TokenCache(K, V, lengths=i32(lens), weights=torch.zeros(B, Hkv, T, device="cuda"))
+        dec = steps.SharedPrefixDecoder(cache, Hq=Hkv * G, Kp=Kp, Vp=Vp, group_start=i32([0, 16]))
+        out, lse = dec.attend(q)
+        csa.csa_check_device_status()
+        return out.clone(), lse.clone(), cache.weights.clone()
+
+    want = run()
+    q[3, G + 1, 5] = float("nan")           # one row
+    K[17, 1, 77, 0] = float("nan")          # the rows of one sequence and KV head
+    K[18, 0, 3] = float("inf")
+    got = run()
+    bad = torch.zeros(B, Hkv * G, dtype=torch.bool, device="cuda")
+    bad[3, G + 1] = True
+    bad[17, G:] = True
+    # K = inf in all D: q.k is a sum of both infinities, or all of one sign by chance
+    free = torch.ones(B, Hkv * G, dtype=torch.bool, device="cuda")
+    free[18, :G] = False
+    assert bool(torch.isnan(got[1][bad]).all()) and bool(torch.isnan(got[0][bad]).all())
+    keep = ~bad & free
+    assert torch.equal(got[1][keep], want[1][keep]) and torch.equal(got[0][keep], want[0][keep])
+    assert bool(torch.isnan(got[2][17, 1]).all()) and torch.equal(got[2][17, 0], want[2][17, 0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_many_sequences(steps, csa, dtype):
+    """More sequences than the threads of a block: the split takes several rounds."""
+    B = 700
+    lens = [(i * 37) % 34 for i in range(B)]
+    _decode_check(steps, csa, dtype, B, 1, 2, 64, 3, 90, 33, [90, 0, 41], [0, 300, 301, 690], lens, seed=2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_broadcast_storage(steps, csa, dtype):
+    """Keys and values stored once for all heads, or for all sequences."""
+    B, Hkv, G, D, T, Tp = 3, 4, 4, 128, 90, 150
+    dt = DT[dtype]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    q = _randn((B, Hkv * G, D), 1, dt)
+    Kp, Vp = (_randn((1, 1, Tp, D), s, dt).expand(1, Hkv, Tp, D) for s in (2, 3))
+    K, V = (_randn((1, Hkv, T, D), s, dt).expand(B, Hkv, T, D) for s in (4, 5))
+
+    def run(*kv):
+        cache = steps.TokenCache(kv[0], kv[1], lengths=i32([90, 17, 64]))
+        dec = steps.SharedPrefixDecoder(cache, Hq=Hkv * G, Kp=kv[2], Vp=kv[3])
+        out, lse = dec.attend(q)
+        csa.csa_check_device_status()
+        return out.clone(), lse.clone(), cache.weights.clone()
+
+    for x, y in zip(run(K, V, Kp, Vp), run(*(t.contiguous() for t in (K, V, Kp, Vp)))):
+        assert torch.equal(x, y)
+
+
+def test_offsets_beyond_32_bits(steps, csa):
+    """Keys and values of more than 2^31 elements: prefix, own cache, insert and
+    compress at their far ends."""
+    H, T, D = 2, 8_500_000, 128
+    K = torch.zeros(1, H, T, D, dtype=torch.bfloat16, device="cuda")
+    V = torch.zeros_like(K)
+    q = _randn((1, 8, D), 1, torch.bfloat16)
+    spots = [0, T // 2 + 3, T - 1]
+    for i, t in enumerate(spots):
+        K[0, :, t] = (q[0, ::4] * (1 + 0.01 * i)).to(torch.bfloat16)
+        V[0, :, t] = _randn((H, D), 20 + i, torch.bfloat16)
+    # T keys of logit 0 (less the spots), and the spots
+    qd = q[0].double().view(H, 4, D)
+    logits = torch.stack([torch.einsum("hgd,hd->hg", qd, K[0, :, t].double()) / D ** 0.5 for t in spots], -1)
+    for as_prefix in (False, True):
+        if as_prefix:
+            cache = steps.TokenCache(K[:, :, :1], V[:, :, :1])
+            dec = steps.SharedPrefixDecoder(cache, Hq=8, Kp=K, Vp=V)
+        else:
+            cache = steps.TokenCache(K, V, lengths=torch.tensor([T], dtype=torch.int32, device="cuda"), n_local=4)
+            dec = steps.SharedPrefixDecoder(cache, Hq=8)
+        out, lse = dec.attend(q)
+        csa.csa_check_device_status()
+        want = torch.logsumexp(torch.cat([logits, torch.full((H, 4, 1), math.log(T - 3), device="cuda")], -1), -1)
+        # a partial's sum takes at most 2^12 steps, each off by 2^-24 of it: 2.5e-4 of l, of a weight and of lse
+        assert (lse[0].view(H, 4) - want).abs().max() < 1e-3
+        p = (logits - want[..., None]).exp()
+        ref = torch.einsum("hgs,hsd->hgd", p, torch.stack([V[0, :, t].double() for t in spots], 1))
+        size = torch.einsum("hgs,hsd->hgd", p, torch.stack([V[0, :, t].double().abs() for t in spots], 1))
+        assert bool(((out[0].view(H, 4, D).double() - ref).abs() <= (U16 + 4e-3) * size + 1e-6).all())
+    assert (cache.weights.numel() == H)  # the prefix run's own cache; the first one's is below
+    cache = steps.TokenCache(K, V, lengths=torch.tensor([T], dtype=torch.int32, device="cuda"),
+                             next_pos=torch.tensor([T], dtype=torch.int32, device="cuda"), n_local=2)
+    cache.positions.copy_(torch.arange(T, dtype=torch.int32, device="cuda").expand(1, H, T))
+    cache.weights.fill_(1.0)
+    cache.weights[0, :, T - 3] = 0.5
+    k, v = _randn((1, H, D), 30, torch.bfloat16), _randn((1, H, D), 31, torch.bfloat16)
+    cache.insert(k, v)
+    csa.csa_check_device_status()
+    assert torch.equal(K[0, :, T - 3], k[0]) and torch.equal(V[0, :, T - 3], v[0])
+    assert cache.positions[0, :, T - 3].tolist() == [T, T]
+    small = steps.TokenCache(*(torch.zeros(1, H, 8, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)), n_sink=1, n_local=2)
+    w = torch.rand(1, H, T, device="cuda")
+    small.compress(K, V, w)
+    csa.csa_check_device_status()
+    for h in range(H):
+        top = torch.sort(w[0, h, 1:T - 2], descending=True, stable=True)[1][:5] + 1
+        rows = sorted([0, T - 2, T - 1] + top.tolist())
+        assert small.positions[0, h].tolist() == rows
+        assert torch.equal(small.K[0, h], K[0, h, rows]) and torch.equal(small.V[0, h], V[0, h, rows])
+
+
+def test_rotary_offsets_beyond_32_bits(steps):
+    S, H, D = 131072, 160, 128
+    x = torch.zeros(1, S, H, D, dtype=torch.bfloat16, device="cuda")
+    x[:, -3:] = _randn((1, 3, H, D), 4, torch.bfloat16)
+    before = x[:, -3:].clone()
+    steps.Rotary(128).rotate(x, q_out=x)
+    _rotary_close(x[:, -3:], before, np.arange(S - 3, S)[None], oracle_freqs(128, 10000.0), "half", 1.0, False)
+    assert not x[:, :-3].any()
+
+
+def test_empty_batches(steps, csa):
+    K = torch.zeros(0, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    cache = steps.TokenCache(K, K.clone())
+    cache.insert(K[:, :, 0], K[:, :, 0])
+    cache.compress(K, K.clone(), torch.zeros(0, 2, 16, device="cuda"))
+    out, lse = steps.SharedPrefixDecoder(cache, Hq=4).attend(torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda"))
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    csa.csa_check_device_status()
+
+
+def test_rotary_outputs_belong_to_the_stream(steps, csa):
+    """Without outputs, a torch stream allocates them; a raw one needs them."""
+    x = _randn((2, 5, 3, 64), 1)
+    r = steps.Rotary(64)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = r.rotate(x, pos0=7, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, r.rotate(x, pos0=7))
+    with pytest.raises(csa.CsaError):
+        r.rotate(x, stream=side.cuda_stream)
+    with pytest.raises(csa.CsaError):
+        r.rotate(x.half())
+    with pytest.raises(csa.CsaError):
+        steps.TokenCache(x.half(), x.half())

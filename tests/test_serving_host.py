@@ -196,13 +196,13 @@ def test_compress_refusals(csa):
     (dict(N=65), UNSUPPORTED, "N must be"), (dict(B=1 << 16), UNSUPPORTED, "65535"),
     (dict(scale=float("inf")), INVALID, "scale"), (dict(scale=0.0), INVALID, "scale"),
     (dict(decay=-1.0), INVALID, "decay"), (dict(N=2), INVALID, "group_start"), (dict(out_dtype=4), INVALID, "out_dtype"),
-    (dict(kp_stride=(8, 8, 4)), UNSUPPORTED, "Kp: strides"), (dict(v_stride=(-8, 8, 8)), INVALID, "V: strides"),
+    (dict(kp_stride=(8, 4, 128)), UNSUPPORTED, "Kp: strides"), (dict(kp_stride=(8, 8, 0)), UNSUPPORTED, "Kp: strides"), (dict(v_stride=(-8, 8, 128)), INVALID, "V: strides"),
     (dict(T=1 << 31), UNSUPPORTED, "Tp and T"), (dict(B=4096, T=1 << 30), UNSUPPORTED, "too many keys"),
     (dict(N=0, T=0), INVALID, "q is NULL"), (dict(), INVALID, "Kp is NULL"),
 ])
 def test_prefix_decode_refusals(csa, change, status, word):
     kw = dict(dtype=1, B=2, Hq=8, Hkv=2, D=128, scale=0.1, N=1, Tp=128, T=64, decay=1.0)
-    kw.update({f"{n}_stride": (0, 0, 0) for n in ("kp", "vp", "k", "v")})
+    kw.update({f"{n}_stride": (0, 0, 128) for n in ("kp", "vp", "k", "v")})
     kw.update(change)
     d = csa.prefix_decode_desc(**kw)
     if word == "V: strides":  # the prefix's pointers come first
@@ -223,6 +223,7 @@ def test_binding_checks_tensors():
                 lambda: steps._rows("x", x, torch.bfloat16),
                 lambda: steps._dense("x", x.transpose(0, 1), torch.float32, (3, 2, 4, 8)),
                 lambda: steps._dense("x", x, torch.float32, (2, 3, 4, 9)),
-                lambda: steps._same_device(torch.device("cpu"), x=x.to("meta"))):
+                lambda: steps._same_device(torch.device("cpu"), x=x.to("meta")),
+                lambda: steps._typed("x", torch.float16), lambda: steps._empty_like(x, 5)):
         with pytest.raises(csa.CsaError):
             bad()
