@@ -21,17 +21,22 @@ namespace {
 
 // ------------------------------------------------------------------ fp32
 //
-// Plain fp32 products on the FMA pipe: a tile of 32 query rows against chunks
-// of 32 keys held in shared memory, a thread four rows by two keys of the logits
-// and four rows by D/16 columns of the output.  Bound: with few rows HBM (a
-// chunk is 256 D bytes), with 32 the FMA pipe (2 * 32 * 32 * D products a
-// chunk).  Small chunks and CTAs, four per SM: the loads of one hide under
-// the products of the others, and a short batch still fills the SMs (one
-// chunk of 64 keys on 256 threads, two CTAs per SM: 35 us for 8 sequences over
-// 4K tokens).
+// Plain fp32 products on the FMA pipe: a tile of up to 32 query rows against
+// chunks of 32 keys held in shared memory.  Bound: with few rows HBM (a chunk
+// is 256 D bytes), with 32 the FMA pipe (2 * 32 * 32 * D products a chunk).
+// For the logits each warp takes a quarter of D for the whole tile, a thread up
+// to eight rows by four keys (12 loads from shared memory to 128 products; four
+// by two with all of D in each warp: 6 to 32, bound by those loads), and the
+// quarters meet in shared memory, on the keys that have been read.  Rows and
+// keys are dealt out in turn, so that a tile of few rows still has every warp
+// at work.  Four workers of four warps to a CTA, one CTA per SM: the loads of
+// one hide under the products of the others, and a short batch still fills
+// the SMs.  8 sequences of 16 heads over 4K tokens and 511 own keys each: 32 us
+// with the merge, about 23 here: 2 to the split, 4 for the first chunks (25 MB,
+// all workers' at once), then one or two chunks a worker, 3 to 6 us each.
 constexpr int kF32Rows = 32;
 constexpr int kF32Threads = 128;
-constexpr int kF32Ctas = 4;  // per SM
+constexpr int kF32Workers = 4;  // per CTA, one CTA per SM
 constexpr int kF32ChunkLog2 = 5, kF32Chunk = 1 << kF32ChunkLog2;
 constexpr int kF32Lead = 1;  // a unit's queries and partials, in chunks' time
 
@@ -44,26 +49,119 @@ __device__ __forceinline__ void copy16(uint32_t dst, const float* src, bool in) 
                : "memory");
 }
 
+// A barrier of one worker's threads.
+__device__ __forceinline__ void f32_meet(int worker) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "n"(kF32Threads) : "memory");
+}
+
+// Floats of shared memory of a worker: queries, values, weights, keys (the
+// logits' quarters later).
+__host__ __device__ constexpr int f32_floats(int D) {
+  return kF32Rows * (D + 4) + kF32Chunk * D + kF32Rows * kF32Chunk +
+         (D > 4 * kF32Rows - 4 ? kF32Chunk * (D + 4) : 4 * kF32Rows * kF32Chunk);
+}
+
+// Place of (row, key) in a tile of weights, 32 floats a row: rows of equal
+// number mod 4 are turned alike, so that neither a thread's four keys nor
+// a row's eight in sequence meet on a bank.
+__device__ __forceinline__ int f32_place(int row, int key) {
+  return row * kF32Chunk + ((key + 8 * (row & 3)) & (kF32Chunk - 1));
+}
+
+// This warp's quarter of D of the logits of rows 0 .. 4 RI - 1, into red once
+// every warp has read the keys it lies on.
+template <int D, int RI>
+__device__ __forceinline__ void f32_logits(const float* sq, const float* sk, float* red, int worker,
+                                           int warp, int lane) {
+  constexpr int KS = D + 4;
+  const int rg = lane >> 3, kg = lane & 7;
+  const float* qa = sq + rg * KS + warp * (D / 4);
+  const float* ka = sk + kg * KS + warp * (D / 4);
+  float s[RI][4] = {};
+#pragma unroll 2
+  for (int d = 0; d < D / 4; d += 4) {
+    float4 k[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) k[c] = ld4(ka + 8 * c * KS + d);
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      const float4 a = ld4(qa + 4 * i * KS + d);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        s[i][c] = fmaf(a.w, k[c].w, fmaf(a.z, k[c].z, fmaf(a.y, k[c].y, fmaf(a.x, k[c].x, s[i][c]))));
+    }
+  }
+  f32_meet(worker);
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      red[warp * kF32Rows * kF32Chunk + f32_place(rg + 4 * i, kg + 8 * c)] = s[i][c];
+}
+
+// o += weights * v for rows ty + 8 i, i < RO, columns 64 e + 4 tx ...
+template <int D, int RO>
+__device__ __forceinline__ void f32_values(const float* ss, const float* al, const float* sv, int tx,
+                                           int ty, float (&o)[kF32Rows / 8][D / 16]) {
+#pragma unroll
+  for (int r = 0; r < RO; ++r) {
+    const float f = al[ty + 8 * r];
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) o[r][d] *= f;
+  }
+#pragma unroll 2
+  for (int t = 0; t < kF32Chunk; t += 4) {
+    float4 pw[RO];
+#pragma unroll
+    for (int r = 0; r < RO; ++r) pw[r] = ld4(ss + f32_place(ty + 8 * r, t));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) {
+        const float4 v = ld4(sv + (t + k) * D + d * 64 + tx * 4);
+#pragma unroll
+        for (int r = 0; r < RO; ++r) {
+          const float w = k == 0 ? pw[r].x : k == 1 ? pw[r].y : k == 2 ? pw[r].z : pw[r].w;
+          o[r][4 * d] += w * v.x;
+          o[r][4 * d + 1] += w * v.y;
+          o[r][4 * d + 2] += w * v.z;
+          o[r][4 * d + 3] += w * v.w;
+        }
+      }
+  }
+}
+
 template <int D>
-__global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams p) {
-  constexpr int KS = D + 4, SS = kF32Chunk + 4;
+__global__ void __launch_bounds__(kF32Workers* kF32Threads) attend_f32_kernel(const PdParams p) {
+  constexpr int KS = D + 4;
   constexpr int D4 = D / 4;
+  static_assert(kF32Threads == 4 * kF32Rows);
   extern __shared__ __align__(16) float sm[];
-  float* sq = sm;                           // [32][KS]
-  float* sk = sq + kF32Rows * KS;           // [32][KS]
-  float* sv = sk + kF32Chunk * KS;          // [32][D]
-  float* ss = sv + kF32Chunk * D;           // [32][SS]
+  const int worker = threadIdx.x / kF32Threads;
+  float* sq = sm + worker * f32_floats(D);  // [32][KS]
+  float* sv = sq + kF32Rows * KS;           // [32][D]
+  float* ss = sv + kF32Chunk * D;           // [32][32], the weights
+  float* sk = ss + kF32Rows * kF32Chunk;    // [32][KS]; then [4][32][32]: the logits' quarters
+  float* red = sk;
   __shared__ int gs[kPdMaxPrefixes + 1];
   __shared__ PdStart st[8];
-  __shared__ uint64_t scan_sh[kF32Threads / 32];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  __shared__ uint64_t scan_sh[kF32Workers * kF32Threads / 32];
+  __shared__ float factors[kF32Workers][kF32Rows];  // of each row's output, a chunk's
+  float* al = factors[worker];
+  const int tid = threadIdx.x % kF32Threads, warp = tid >> 5, lane = tid & 31;
+  const int tx = tid & 15, ty = tid >> 4;
+  const int row = tid >> 2, key8 = (tid & 3) * 8;  // of the softmax
   const PdShape& shape = p.b.s;
   pdl_next();  // the merge
-  const int key0 = tid < shape.N + shape.B ? pd_raw_keys(shape, tid) : 0;
-  if (tid < 32) pd_groups(shape, gs);
+  const int item = static_cast<int>(threadIdx.x);
+  const int key0 = item < shape.N + shape.B ? pd_raw_keys(shape, item) : 0;
+  if (item < 32) pd_groups(shape, gs);
   __syncthreads();
   pd_locate(p.a.s, shape, gs, key0, st, scan_sh, nullptr, blockIdx.x == 0 ? &p.b.plan : nullptr);
-  PdWalk walk(shape, gs, st[0]);
+  // from here on each worker by itself, with a barrier of its own
+  auto meet = [worker] { f32_meet(worker); };
+  PdWalk walk(shape, gs, st[worker]);
+  const int64_t number = static_cast<int64_t>(worker) * gridDim.x + blockIdx.x;
   PdSeg g;
   while (walk.next(g)) {
     const int64_t* kst = g.own ? p.ks : p.kps;
@@ -72,115 +170,133 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const PdParams 
     const float* Kg = static_cast<const float*>(g.own ? p.K : p.Kp) + k0 * kst[0] + g.h * kst[1];
     const float* Vg = static_cast<const float*>(g.own ? p.V : p.Vp) + k0 * vst[0] + g.h * vst[1];
     const float* q = static_cast<const float*>(p.q);
-    for (int i = tid; i < kF32Rows * D4; i += kF32Threads) {
-      const int r = i / D4, d = (i % D4) * 4;
-      const int row = g.row0 + r, b = row / shape.G, hd = g.h * shape.G + row % shape.G;
-      const bool in = r < g.rows;
-      copy16(smem_u32(sq + r * KS + d), in ? q + (static_cast<int64_t>(b) * p.Hq + hd) * D + d : q, in);
-    }
-    // warps whose rows are past the unit's only help with the loads
-    const bool active = (ty & ~1) * 4 < g.rows;
-    float m[4], l[4], o[4][D / 16];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) o[r][d] = 0.f;
-    }
-    for (int j = g.j0; j < g.j1; ++j) {
+    // a chunk's rows; those past the keys are zero: whatever the cache holds
+    // there, 0 * v stays 0
+    auto load = [&](float* to, int ld, const float* from, int64_t stride, int j) {
       const int t0 = j * kF32Chunk, nk = min(kF32Chunk, g.keys - t0);
-      // rows past the keys are zero: whatever the cache holds there, 0 * v stays 0
 #pragma unroll 4
       for (int i = tid; i < kF32Chunk * D4; i += kF32Threads) {
         const int t = i / D4, d = (i % D4) * 4;
-        copy16(smem_u32(sk + t * KS + d), t < nk ? Kg + (t0 + t) * kst[2] + d : q, t < nk);
-        copy16(smem_u32(sv + t * D + d), t < nk ? Vg + (t0 + t) * vst[2] + d : q, t < nk);
+        copy16(smem_u32(to + t * ld + d), t < nk ? from + (t0 + t) * stride + d : q, t < nk);
       }
-      asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
-      __syncthreads();
-      if (active) {
-        float s[4][2] = {};
-#pragma unroll 4
-        for (int d = 0; d < D; d += 4) {
-          float4 a[4], k[2];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) a[r] = ld4(sq + (ty * 4 + r) * KS + d);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) k[c] = ld4(sk + (tx + 16 * c) * KS + d);
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              s[r][c] += a[r].x * k[c].x + a[r].y * k[c].y + a[r].z * k[c].z + a[r].w * k[c].w;
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = ty * 4 + r;
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            s[r][c] = tx + 16 * c < nk ? s[r][c] * p.scale_log2 : -INFINITY;
-          if (g.own && p.logits && row < g.rows) {
-            float* lg = p.logits + (static_cast<int64_t>(g.unit) * shape.G + row) * p.Tl + t0;
-            lg[tx] = s[r][0];
-            lg[tx + 16] = s[r][1];
-          }
-          float mx = fmaxf(s[r][0], s[r][1]);
-#pragma unroll
-          for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn;
-          const float al = exp2f(m[r] - base);
-          const float e0 = exp2f(s[r][0] - base), e1 = exp2f(s[r][1] - base);
-          ss[row * SS + tx] = e0;
-          ss[row * SS + tx + 16] = e1;
-          float sum = e0 + e1;
-#pragma unroll
-          for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-          l[r] = l[r] * al + sum;
-          m[r] = mn;
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d) o[r][d] *= al;
-        }
-        __syncwarp();  // a row's weights are written and read by the same half-warp
-#pragma unroll 2
-        for (int t = 0; t < kF32Chunk; t += 4) {
-          float4 pw[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) pw[r] = ld4(ss + (ty * 4 + r) * SS + t);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int d = 0; d < D / 64; ++d) {
-              const float4 v = ld4(sv + (t + k) * D + d * 64 + tx * 4);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float w = k == 0 ? pw[r].x : k == 1 ? pw[r].y : k == 2 ? pw[r].z : pw[r].w;
-                o[r][4 * d] += w * v.x;
-                o[r][4 * d + 1] += w * v.y;
-                o[r][4 * d + 2] += w * v.z;
-                o[r][4 * d + 3] += w * v.w;
-              }
-            }
-        }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    {
+      constexpr int kStep = kF32Threads / D4;  // rows from one pass to the next
+      const int r0 = tid / D4, d = tid % D4 * 4;
+      int b = (g.row0 + r0) / shape.G, hd = g.row0 + r0 - b * shape.G;
+      for (int r = r0; r < kF32Rows; r += kStep) {
+        const bool in = r < g.rows;
+        const int64_t row = static_cast<int64_t>(b) * p.Hq + g.h * shape.G + hd;
+        copy16(smem_u32(sq + r * KS + d), in ? q + row * D + d : q, in);
+        for (hd += kStep; hd >= shape.G; hd -= shape.G) ++b;
       }
-      __syncthreads();  // the chunk, and after the last one the queries, have been read
     }
-    if (!active) continue;
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) + g.unit;
+    load(sk, KS, Kg, kst[2], g.j0);
+    load(sv, D, Vg, vst[2], g.j0);
+    float m = -INFINITY, l = 0.f;
+    float o[kF32Rows / 8][D / 16];
+#pragma unroll
+    for (int r = 0; r < kF32Rows / 8; ++r)
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) o[r][d] = 0.f;
+    for (int j = g.j0; j < g.j1; ++j) {
+      const int t0 = j * kF32Chunk, nk = min(kF32Chunk, g.keys - t0);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");  // the keys
+      meet();
+      if (g.rows <= 4)
+        f32_logits<D, 1>(sq, sk, red, worker, warp, lane);
+      else if (g.rows <= 8)
+        f32_logits<D, 2>(sq, sk, red, worker, warp, lane);
+      else if (g.rows <= 16)
+        f32_logits<D, 4>(sq, sk, red, worker, warp, lane);
+      else
+        f32_logits<D, 8>(sq, sk, red, worker, warp, lane);
+      meet();
+      if (warp * 8 < g.rows) {
+        // four threads a row, eight keys each; odd rows take their second four
+        // first (no bank twice)
+        float s[8];
+        const int at = f32_place(row, key8), odd = (row & 1) * 4;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row < g.rows)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float4 y = ld4(red + w * kF32Rows * kF32Chunk + at + (e ^ odd));
+              x.x += y.x;
+              x.y += y.y;
+              x.z += y.z;
+              x.w += y.w;
+            }
+          const int k = key8 + (e ^ odd);
+          s[e] = k < nk ? x.x * p.scale_log2 : -INFINITY;
+          s[e + 1] = k + 1 < nk ? x.y * p.scale_log2 : -INFINITY;
+          s[e + 2] = k + 2 < nk ? x.z * p.scale_log2 : -INFINITY;
+          s[e + 3] = k + 3 < nk ? x.w * p.scale_log2 : -INFINITY;
+          if (g.own && p.logits && row < g.rows)
+            *reinterpret_cast<float4*>(
+                p.logits + (static_cast<int64_t>(g.unit) * shape.G + row) * p.Tl + t0 + k) =
+                make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s[e] = exp2f(s[e] - base);
+          sum += s[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 4)
+          *reinterpret_cast<float4*>(ss + at + (e ^ odd)) =
+              make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        l = l * f + sum;
+        m = mn;
+        if ((tid & 3) == 0) al[row] = f;
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");  // the values
+      meet();
+      // the next keys under the products, the next values behind them
+      const bool more = j + 1 < g.j1;
+      if (more) load(sk, KS, Kg, kst[2], j + 1);
+      if (g.rows <= 8) {
+        if (ty < g.rows) f32_values<D, 1>(ss, al, sv, tx, ty, o);
+      } else if (g.rows <= 16) {
+        f32_values<D, 2>(ss, al, sv, tx, ty, o);
+      } else {
+        f32_values<D, 4>(ss, al, sv, tx, ty, o);
+      }
+      meet();  // the chunk, and after the last one the queries, have been read
+      if (more) load(sv, D, Vg, vst[2], j + 1);
+    }
+    const int64_t slot = number + g.unit;
     const int rows = g.own ? shape.G : p.b.slot_rows;
     float* po = (g.own ? p.oo : p.b.po) + slot * rows * D;
     float* pl = (g.own ? p.olse : p.b.plse) + slot * rows;
+    if (row < g.rows && (tid & 3) == 0) {
+      al[row] = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
+      pl[row] = l == 0.f ? -INFINITY : m + log2f(l);
+    }
+    meet();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = ty * 4 + r;
-      if (row < g.rows) {
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];  // a NaN stays one
+    for (int r = 0; r < kF32Rows / 8; ++r) {
+      const int orow = ty + 8 * r;
+      if (orow < g.rows) {
+        const float inv = al[orow];
 #pragma unroll
         for (int d = 0; d < D / 64; ++d)
-          *reinterpret_cast<float4*>(po + static_cast<int64_t>(row) * D + d * 64 + tx * 4) =
+          *reinterpret_cast<float4*>(po + static_cast<int64_t>(orow) * D + d * 64 + tx * 4) =
               make_float4(o[r][4 * d] * inv, o[r][4 * d + 1] * inv, o[r][4 * d + 2] * inv,
                           o[r][4 * d + 3] * inv);
-        if (tx == 0) pl[row] = l[r] == 0.f ? -INFINITY : m[r] + log2f(l[r]);
       }
     }
   }
@@ -469,8 +585,10 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
     p->b.slot_rows = b.R;
   } else {
     b.R = kF32Rows;
-    b.ctas = kF32Ctas * num_sms;
-    b.workers = 1;
+    b.ctas = num_sms;
+    b.workers = kF32Workers;
+    // the line's front (prefixes, many rows) is the dearer part: some on every SM
+    b.spread = 1;
     b.chunk_log2 = kF32ChunkLog2;
     b.lead = kF32Lead;
     b.max_rows = 1 << 30;
@@ -493,11 +611,11 @@ int64_t pd_layout(PdParams* p, char* ws, bool bf16, int B, int Hkv, int G, int D
 
 template <int D>
 cudaError_t launch_attend_f32(const Launch& l, const PdParams& p) {
-  const int smem = ((kF32Rows + kF32Chunk) * (D + 4) + kF32Chunk * D + kF32Rows * (kF32Chunk + 4)) * 4;
+  const int smem = kF32Workers * f32_floats(D) * 4;
   cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attend_f32_kernel<D><<<p.b.s.ctas, kF32Threads, smem, l.stream>>>(p);
+  attend_f32_kernel<D><<<p.b.s.ctas, kF32Workers * kF32Threads, smem, l.stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -41,6 +41,7 @@ struct PdShape {
   float inv_R;
   int ctas;                    // CTAs that the lines share (0: no such line)
   int workers;                 // workers per CTA, at most 8
+  int spread;                  // worker k of CTA c is number c + k * CTAs (0: c * workers + k)
   int chunk_log2;              // keys per chunk
   int lead;                    // places before a unit's chunks
   int min_rows, max_rows;      // prefix units of groups of so many rows
@@ -219,13 +220,16 @@ __device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b,
   const PdShape& me = on_a ? a : b;
   const int block = static_cast<int>(blockIdx.x) - (on_a ? 0 : na);
   const int W = on_a ? Wa : Wb, P = on_a ? Pa : Pb, nw = me.workers;
-  const int x_lane = pd_cut(W, min(P, block * nw + min(lane, nw)), P);  // lane k: worker k's start
+  // lane k: worker k's bounds
+  const int wk = min(lane, nw);
+  const int c_lane = me.spread ? wk * b.ctas + block : block * nw + wk;
+  const int x_lane = pd_cut(W, min(P, c_lane), P), xe_lane = pd_cut(W, min(P, c_lane + 1), P);
   auto place = [&](int i, uint64_t at, uint64_t mine) {
     const int e = static_cast<int>(on_a ? at >> 32 : at & 0xffffffffu);
     const int n = static_cast<int>(on_a ? mine >> 32 : mine & 0xffffffffu);
 #pragma unroll 1
     for (int k = 0; k < nw; ++k) {
-      const int x0 = __shfl_sync(0xffffffffu, x_lane, k), x1 = __shfl_sync(0xffffffffu, x_lane, k + 1);
+      const int x0 = __shfl_sync(0xffffffffu, x_lane, k), x1 = __shfl_sync(0xffffffffu, xe_lane, k);
       if (x1 > x0 && x0 >= e && x0 < e + n) {  // places [e, e + n) are item i's
         st[k].left = x1 - x0;
         st[k].item = i;
