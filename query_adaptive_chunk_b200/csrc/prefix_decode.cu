@@ -144,8 +144,7 @@ __global__ void __launch_bounds__(kF32Workers* kF32Threads) attend_f32_kernel(co
   float* sk = ss + kF32Rows * kF32Chunk;    // [32][KS]; then [4][32][32]: the logits' quarters
   float* red = sk;
   __shared__ int gs[kPdMaxPrefixes + 1];
-  __shared__ PdStart st[8];
-  __shared__ uint64_t scan_sh[kF32Workers * kF32Threads / 32];
+  __shared__ PdShared ps;
   __shared__ float factors[kF32Workers][kF32Rows];  // of each row's output, a chunk's
   float* al = factors[worker];
   const int tid = threadIdx.x % kF32Threads, warp = tid >> 5, lane = tid & 31;
@@ -157,10 +156,10 @@ __global__ void __launch_bounds__(kF32Workers* kF32Threads) attend_f32_kernel(co
   const int key0 = item < shape.N + shape.B ? pd_raw_keys(shape, item) : 0;
   if (item < 32) pd_groups(shape, gs);
   __syncthreads();
-  pd_locate(p.a.s, shape, gs, key0, st, scan_sh, nullptr, blockIdx.x == 0 ? &p.b.plan : nullptr);
+  pd_locate(p.a.s, shape, gs, key0, &ps, nullptr, blockIdx.x == 0 ? &p.b.plan : nullptr);
   // from here on each worker by itself, with a barrier of its own
   auto meet = [worker] { f32_meet(worker); };
-  PdWalk walk(shape, gs, st[worker]);
+  PdWalk walk(shape, gs, ps.st[worker]);
   const int64_t number = static_cast<int64_t>(worker) * gridDim.x + blockIdx.x;
   PdSeg g;
   while (walk.next(g)) {

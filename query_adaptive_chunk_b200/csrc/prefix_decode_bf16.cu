@@ -23,8 +23,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   __shared__ int gs[kPdMaxPrefixes + 1];
-  __shared__ PdStart st[kPdWarps];
-  __shared__ uint64_t scan_sh[kTcThreads / 32];
+  __shared__ PdShared ps;
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5;
   const bool two = p.a.s.ctas > 0;
@@ -43,12 +42,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const bool first = blockIdx.x == 0;
-  const PdPlace at = pd_locate(p.a.s, p.b.s, gs, key0, st, scan_sh,
+  const PdPlace at = pd_locate(p.a.s, p.b.s, gs, key0, &ps,
                                first && two ? &p.a.plan : nullptr, first ? &p.b.plan : nullptr);
   if (at.line == 0)
-    attend_tc<D>(tmK, tmV, tmQ, tmQs, tmO, mp, p, smem, bars, tmem_slot, gs, st[0], at.block);
+    attend_tc<D>(tmK, tmV, tmQ, tmQs, tmO, mp, p, smem, bars, tmem_slot, gs, ps.st[0], at.block);
   if (two && warp == 1) tmem_dealloc<512>(tmem_slot);
-  if (at.line == 1 && warp < kPdWarps) attend_warp<D, NT>(p, smem, gs, st, at.block);
+  if (at.line == 1 && warp < kPdWarps) attend_warp<D, NT>(p, smem, gs, ps.st, at.block);
 }
 
 // A tensor map of [n0, n1, rows, D]; a dimension of one entry, or of stride 0

@@ -116,9 +116,16 @@ __device__ __forceinline__ void pd_groups(const PdShape& s, int* gs) {
 }
 
 // A worker's stretch of the line: `left` places from place `off` of item `item`
-// on; unit0 prefix units lie before it (prefix items only).
+// (of `keys` keys) on; unit0 prefix units lie before it (prefix items only).
 struct PdStart {
-  int left, item, off, unit0;
+  int left, item, off, unit0, keys;
+};
+
+// Shared memory of pd_locate: its result, and the scan's.
+struct PdShared {
+  PdStart st[8];       // the CTA's workers' stretches
+  uint64_t scan[16];   // one entry per warp
+  int na;              // CTAs on line a
 };
 
 // What the merge needs to find a unit's partials, written by one CTA.
@@ -129,27 +136,29 @@ struct PdPlan {
   int32_t* group;   // [B] each sequence's prefix, or -1 (line b's plan)
 };
 
-// Exclusive prefix sum over the block of two counts packed in 64 bits, one
-// barrier; `sh` holds one entry per warp.
-__device__ __forceinline__ uint64_t pd_scan(uint64_t v, uint64_t* sh, uint64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+// Exclusive prefix sum over the block's first `warps` warps of two counts packed
+// in 64 bits; `sh` holds one entry per warp.  Every thread of the block calls it.
+__device__ __forceinline__ uint64_t pd_scan(uint64_t v, uint64_t* sh, int warps, uint64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t x = v;
+  if (warp < warps) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
   }
-  if (lane == 31) sh[warp] = x;
   __syncthreads();
-  uint64_t w = lane < nw ? sh[lane] : 0;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += y;
+  uint64_t before = 0, all = 0;
+#pragma unroll 4
+  for (int w = 0; w < warps; ++w) {
+    const uint64_t y = sh[w];
+    before += w < warp ? y : 0;
+    all += y;
   }
-  *total = __shfl_sync(0xffffffffu, w, nw - 1);
-  const uint64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-  return (warp > 0 ? before : 0) + x - v;
+  *total = all;
+  return before + x - v;
 }
 
 // Places of W before worker c of P (c <= P <= 2^15).
@@ -164,107 +173,116 @@ struct PdPlace {
   int block;  // its number on that line
 };
 
-// Block-wide: the CTA's line, and st[0 .. 7] (shared), the places of its
-// workers there.  `gs` (shared) is filled by pd_groups before a barrier; key0 =
-// pd_raw_keys of item threadIdx.x, loaded before that barrier (any value for
-// threads past the items).  One CTA passes plans to write.
+// Block-wide: the CTA's line, and ps->st, the places of its workers there.
+// `gs` (shared) is filled by pd_groups before a barrier; key0 = pd_raw_keys of
+// item threadIdx.x, loaded before that barrier (any value for threads past the
+// items).  One CTA passes plans to write.  Only the warps that hold an
+// item take part.
 __device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b, const int* gs,
-                                             int key0, PdStart* st, uint64_t* scan_sh,
-                                             const PdPlan* plan_a, const PdPlan* plan_b) {
+                                             int key0, PdShared* ps, const PdPlan* plan_a,
+                                             const PdPlan* plan_b) {
   const int items = b.N + b.B, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31;
   const bool two = a.ctas > 0;
+  const bool one = items <= nt;  // one item per thread
+  const int warps = one ? (items + 31) >> 5 : nt >> 5;
   auto units = [&](const PdShape& s, int i) -> int {
     return i < s.N ? pd_tiles(s, gs[i + 1] - gs[i]) * s.Hkv : s.own ? s.Hkv : 0;
   };
+  auto keys_of = [&](int i, int raw) { return pd_clamp(raw, i < b.N ? b.Tp : b.T, b.err); };
   // places of item i: line a in the high half, line b in the low one
-  auto weigh = [&](int i, int raw) -> uint64_t {
+  auto weigh = [&](int i, int keys) -> uint64_t {
     if (i >= items) return 0;
-    const int keys = pd_clamp(raw, i < b.N ? b.Tp : b.T, b.err);
     const uint32_t nb = units(b, i) * pd_places(b, keys);
     const uint32_t na = two && i < b.N ? units(a, i) * pd_places(a, keys) : 0;
     return static_cast<uint64_t>(na) << 32 | nb;
   };
   auto raw_of = [&](int i) { return i < items ? pd_raw_keys(b, i) : 0; };
-  if (tid < 8) st[tid].left = 0;
+  if (tid < 8) ps->st[tid].left = 0;
   uint64_t total = 0, v = 0, ex = 0;
-  const bool one = items <= nt;  // one item per thread
+  int keys = 0;
   if (one) {
-    v = weigh(tid, key0);
-    ex = pd_scan(v, scan_sh, &total);
+    if (tid < items) keys = keys_of(tid, key0);
+    v = weigh(tid, keys);
+    ex = pd_scan(v, ps->scan, warps, &total);
   } else {
     for (int i0 = 0; i0 < items; i0 += nt) {
       const int i = i0 + tid;
       uint64_t tot;
-      pd_scan(weigh(i, raw_of(i)), scan_sh, &tot);
+      pd_scan(weigh(i, i < items ? keys_of(i, raw_of(i)) : 0), ps->scan, warps, &tot);
       total += tot;
-      __syncthreads();  // scan_sh is used again
+      __syncthreads();  // the scan's memory is used again
     }
   }
-  const int Wa = static_cast<int>(total >> 32), Wb = static_cast<int>(total & 0xffffffffu);
-  // line a's CTAs: its share of the keys, at least one for each line with work
   int na = 0;
-  if (Wa > 0) {
-    const float ca = Wa * a.cost, cb = Wb * b.cost;
-    const int most = Wb == 0 ? b.ctas : b.ctas - 1;
-    na = Wb == 0 ? most : max(1, min(most, __float2int_rn(b.ctas * ca / (ca + cb))));
-    // units of one length: a whole number of CTAs each, so that none works on two
-    const int u = b.N == 1 ? units(a, 0) : 0;
-    if (u > 0 && na >= u) {
-      na = (na + u / 2) / u * u;
-      if (na > most) na -= u;
+  if (tid >> 5 < warps) {
+    const int Wa = static_cast<int>(total >> 32), Wb = static_cast<int>(total & 0xffffffffu);
+    // line a's CTAs: its share of the keys, at least one for each line with work
+    if (Wa > 0) {
+      const float ca = Wa * a.cost, cb = Wb * b.cost;
+      const int most = Wb == 0 ? b.ctas : b.ctas - 1;
+      const float share = Wb == 0 ? most : __fdividef(b.ctas * ca, ca + cb);
+      na = max(1, min(most, __float2int_rn(share)));
+      // units of one length: a whole number of CTAs each, so that none works on two
+      const int u = b.N == 1 ? units(a, 0) : 0;
+      if (u > 0 && na >= u) {
+        na = max(1, __float2int_rn(__fdividef(static_cast<float>(na), static_cast<float>(u)))) * u;
+        if (na > most) na -= u;
+      }
     }
-  }
-  // each worker that takes part has a place
-  const int Pa = max(1, min(na, Wa)), Pb = max(1, min((b.ctas - na) * b.workers, Wb));
-  const bool on_a = static_cast<int>(blockIdx.x) < na;
-  const PdShape& me = on_a ? a : b;
-  const int block = static_cast<int>(blockIdx.x) - (on_a ? 0 : na);
-  const int W = on_a ? Wa : Wb, P = on_a ? Pa : Pb, nw = me.workers;
-  // lane k: worker k's bounds
-  const int wk = min(lane, nw);
-  const int c_lane = me.spread ? wk * b.ctas + block : block * nw + wk;
-  const int x_lane = pd_cut(W, min(P, c_lane), P), xe_lane = pd_cut(W, min(P, c_lane + 1), P);
-  auto place = [&](int i, uint64_t at, uint64_t mine) {
-    const int e = static_cast<int>(on_a ? at >> 32 : at & 0xffffffffu);
-    const int n = static_cast<int>(on_a ? mine >> 32 : mine & 0xffffffffu);
-#pragma unroll 1
-    for (int k = 0; k < nw; ++k) {
-      const int x0 = __shfl_sync(0xffffffffu, x_lane, k), x1 = __shfl_sync(0xffffffffu, xe_lane, k);
-      if (x1 > x0 && x0 >= e && x0 < e + n) {  // places [e, e + n) are item i's
-        st[k].left = x1 - x0;
-        st[k].item = i;
-        st[k].off = x0 - e;
+    if (tid == 0) ps->na = na;
+    // each worker that takes part has a place
+    const int Pa = max(1, min(na, Wa)), Pb = max(1, min((b.ctas - na) * b.workers, Wb));
+    const bool on_a = static_cast<int>(blockIdx.x) < na;
+    const PdShape& me = on_a ? a : b;
+    const int block = static_cast<int>(blockIdx.x) - (on_a ? 0 : na);
+    const int W = on_a ? Wa : Wb, P = on_a ? Pa : Pb, nw = me.workers;
+    // lane k: worker k's bounds
+    const int wk = min(lane, nw);
+    const int c_lane = me.spread ? wk * b.ctas + block : block * nw + wk;
+    const int x_lane = pd_cut(W, min(P, c_lane), P), xe_lane = pd_cut(W, min(P, c_lane + 1), P);
+    // this warp's 32 items, from item i0 on: lane k looks worker k's first place up
+    // among them (the last item that starts at or before it)
+    auto place = [&](int i0, int n_keys, uint64_t at, uint64_t mine) {
+      const int e = static_cast<int>(on_a ? at >> 32 : at & 0xffffffffu);
+      const int n = static_cast<int>(on_a ? mine >> 32 : mine & 0xffffffffu);
+      int k = 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (__shfl_sync(0xffffffffu, e, k + o) <= x_lane) k += o;
+      const int ek = __shfl_sync(0xffffffffu, e, k), nk = __shfl_sync(0xffffffffu, n, k);
+      const int keys_k = __shfl_sync(0xffffffffu, n_keys, k);
+      if (lane < nw && xe_lane > x_lane && x_lane >= ek && x_lane < ek + nk) {
+        const int i = i0 + k;
         int before = 0;
         if (i < me.N)
           for (int m = 0; m < i; ++m) before += units(me, m);
-        st[k].unit0 = before;
+        ps->st[lane] = PdStart{xe_lane - x_lane, i, x_lane - ek, before, keys_k};
+      }
+    };
+    auto write = [&](int i, uint64_t at) {
+      if (i >= items) return;
+      if (plan_a) plan_a->starts[i] = static_cast<int>(at >> 32);
+      if (plan_b) plan_b->starts[i] = static_cast<int>(at & 0xffffffffu);
+    };
+    if (one) {
+      place(tid & ~31, keys, ex, v);
+      write(tid, ex);
+    } else {
+      uint64_t run = 0;
+      for (int i0 = 0; i0 < items; i0 += nt) {
+        const int i = i0 + tid;
+        uint64_t tot;
+        const int n_keys = i < items ? keys_of(i, raw_of(i)) : 0;
+        const uint64_t w = weigh(i, n_keys);
+        const uint64_t at = run + pd_scan(w, ps->scan, warps, &tot);
+        place(i & ~31, n_keys, at, w);
+        write(i, at);
+        run += tot;
+        __syncthreads();
       }
     }
-  };
-  auto write = [&](int i, uint64_t at) {
-    if (i >= items) return;
-    if (plan_a) plan_a->starts[i] = static_cast<int>(at >> 32);
-    if (plan_b) plan_b->starts[i] = static_cast<int>(at & 0xffffffffu);
-  };
-  if (one) {
-    place(tid, ex, v);
-    write(tid, ex);
-  } else {
-    uint64_t run = 0;
-    for (int i0 = 0; i0 < items; i0 += nt) {
-      const int i = i0 + tid;
-      uint64_t tot;
-      const uint64_t w = weigh(i, raw_of(i));
-      const uint64_t at = run + pd_scan(w, scan_sh, &tot);
-      place(i, at, w);
-      write(i, at);
-      run += tot;
-      __syncthreads();
-    }
-  }
-  auto finish = [&](const PdShape& s, const PdPlan* plan, int Wl, int Pl) {
-    if (plan == nullptr) return;
-    if (tid == 0) {
+    auto finish = [&](const PdShape& s, const PdPlan* plan, int Wl, int Pl) {
+      if (plan == nullptr || tid != 0) return;
       plan->starts[items] = Wl;
       plan->starts[items + 1] = Pl;
       int u = 0;
@@ -272,10 +290,10 @@ __device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b,
         plan->ubase[n] = u;
         u += units(s, n);
       }
-    }
-  };
-  finish(a, plan_a, Wa, Pa);
-  finish(b, plan_b, Wb, Pb);
+    };
+    finish(a, plan_a, Wa, Pa);
+    finish(b, plan_b, Wb, Pb);
+  }
   if (plan_b) {
     if (b.N > 0 && tid <= b.N) plan_b->gsan[tid] = gs[tid];
     for (int q = tid; q < b.B; q += nt) {
@@ -286,7 +304,9 @@ __device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b,
     }
   }
   __syncthreads();
-  return PdPlace{on_a ? 0 : 1, block};
+  na = ps->na;
+  const bool on_a = static_cast<int>(blockIdx.x) < na;
+  return PdPlace{on_a ? 0 : 1, static_cast<int>(blockIdx.x) - (on_a ? 0 : na)};
 }
 
 // One worker's share of one unit.
@@ -307,16 +327,22 @@ struct PdWalk {
   const int* gs;
   int left, item, h = 0, tile = 0, j = 0, unit0;  // j: place in the unit
   int off;                  // places of `item` before the start
-  int keys = 0, tiles = 0;  // of `item`, once loaded
-  bool loaded = false;
+  int keys, tiles;          // of `item`, once loaded
+  bool loaded;
   __device__ __forceinline__ PdWalk(const PdShape& sh, const int* g, const PdStart& st)
-      : s(sh), gs(g), left(st.left), item(st.item), unit0(st.unit0), off(st.off) {}
+      : s(sh), gs(g), left(st.left), item(st.item), unit0(st.unit0), off(st.off), keys(st.keys) {
+    loaded = left > 0;  // the first item has places
+    if (loaded) tiles = tiles_of(item);
+  }
+  __device__ __forceinline__ int tiles_of(int i) const {
+    return i < s.N ? pd_tiles(s, gs[i + 1] - gs[i]) : s.own;
+  }
   __device__ __forceinline__ bool next(PdSeg& q) {
     while (left > 0) {
       if (!loaded) {
         if (item >= s.N + s.B) return false;
         keys = pd_item_keys(s, item);
-        tiles = item < s.N ? pd_tiles(s, gs[item + 1] - gs[item]) : s.own;
+        tiles = tiles_of(item);
         loaded = keys > 0 && tiles > 0;
         if (!loaded) {
           unit0 += tiles * s.Hkv;  // only read for prefixes
