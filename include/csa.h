@@ -696,7 +696,7 @@ CSA_API csa_status csa_rotary(const csa_rotary_desc* d, csa_stream stream);
  *   len        [B] int32: slots in use, 0 .. budget; slots behind stay as they are
  *   next_pos   [B] int32: the next token's position; < 0: the sequence is
  *              inactive and csa_cache_insert leaves it alone
- *   budget <= T < 2^31;  n_sink, n_local >= 0
+ *   budget <= T < 2^31 - 65536;  n_sink, n_local >= 0
  * Protected slots: position < n_sink, or >= next_pos - n_local.  The others
  * rank by weight (NaN counts as -infinity; -0 == +0), equal weights by slot.
  *   D <= 1024;  B * Hkv <= 65535. */
@@ -739,7 +739,7 @@ CSA_API csa_status csa_cache_insert(const csa_cache_desc* c, const void* k,
  *   src K, V by strides (sequence, head, row); weights [B, Hkv, S] fp32;
  *   positions NULL (the row number) or [B, Hkv, S] int32; src_next_pos NULL
  *   (n) or [B], required with positions.  n_sink + n_local <= budget.
- *   Source and cache (len among them) must not overlap.  S < 2^31; c->counters is
+ *   Source and cache (len among them) must not overlap.  S < 2^31 - 65536; c->counters is
  *   not used. */
 typedef struct csa_cache_source {
   const void* K;

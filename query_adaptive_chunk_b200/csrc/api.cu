@@ -1229,7 +1229,8 @@ csa_status cache_checks(const csa_cache_desc* c, bool insert) {
   else
     CSA_REQUIRE(kept <= c->budget, "n_sink + n_local must not exceed budget");
   CSA_SUPPORT(c->D <= 1024, "D must be <= 1024");
-  CSA_SUPPORT(c->T < 2147483648LL, "T must be < 2^31");
+  // (the kernels' steps past the last slot stay within 32 bits)
+  CSA_SUPPORT(c->T < 2147483648LL - 65536, "T must be < 2^31 - 65536");
   CSA_SUPPORT(static_cast<int64_t>(c->B) * c->Hkv <= 65535, "B*Hkv must be <= 65535");
   return CSA_OK;
 }
@@ -1405,7 +1406,7 @@ csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* s
   CSA_TRY(cache_checks(c, false));
   CSA_REQUIRE(s != nullptr, "the source descriptor is NULL");
   CSA_REQUIRE(s->S >= 0, "S must be non-negative");
-  CSA_SUPPORT(s->S < 2147483648LL, "S must be < 2^31");
+  CSA_SUPPORT(s->S < 2147483648LL - 65536, "S must be < 2^31 - 65536");
   CSA_REQUIRE(s->positions == nullptr || s->next_pos != nullptr,
               "source positions need the source's next_pos");
   if (s->len != nullptr) {

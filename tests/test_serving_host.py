@@ -165,7 +165,7 @@ def test_rotary_table_refusals(csa):
 @pytest.mark.parametrize("change,status,word", [
     (dict(budget=0), INVALID, "budget"), (dict(budget=65), INVALID, "budget"), (dict(n_sink=-1), INVALID, "n_sink"),
     (dict(n_sink=32, n_local=32), INVALID, "below budget"), (dict(D=2048), UNSUPPORTED, "D must be"),
-    (dict(T=1 << 31, budget=8), UNSUPPORTED, "T must be"), (dict(B=1 << 15, Hkv=4), UNSUPPORTED, "65535"),
+    (dict(T=1 << 31, budget=8), UNSUPPORTED, "T must be"), (dict(T=(1 << 31) - 65536, budget=8), UNSUPPORTED, "T must be"), (dict(B=1 << 15, Hkv=4), UNSUPPORTED, "65535"),
     (dict(dtype=9), INVALID, "dtype"), (dict(T=0), INVALID, "T positive"), (dict(), INVALID, "K is NULL"),
 ])
 def test_cache_refusals(csa, change, status, word):
@@ -182,7 +182,7 @@ def test_cache_refusals(csa, change, status, word):
 
 def test_compress_refusals(csa):
     d = csa.cache_desc(dtype=1, B=1, Hkv=1, D=64, T=64, budget=64, len=4096)
-    for kw, status, word in [(dict(S=-1), INVALID, "S must be"), (dict(S=1 << 31), UNSUPPORTED, "S must be"),
+    for kw, status, word in [(dict(S=-1), INVALID, "S must be"), (dict(S=1 << 31), UNSUPPORTED, "S must be"), (dict(S=(1 << 31) - 65536), UNSUPPORTED, "S must be"),
                              (dict(S=8, positions=4096), INVALID, "next_pos"), (dict(S=8, len=4096), INVALID, "len")]:
         src = csa.cache_source(**kw)
         assert csa.lib.csa_cache_compress(ctypes.byref(d), ctypes.byref(src), None) == status
