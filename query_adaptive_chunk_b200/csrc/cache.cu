@@ -148,12 +148,17 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
 // Each CTA writes its kept rows, ascending, into the destination's positions
 // (as row numbers; the copy turns them into positions).  Each warp takes a run of
 // consecutive keys, four a lane (histograms by atomics on one copy per warp; a
-// match of equal buckets first took four times as long).  The weights are read
-// once, sixteen a thread in flight; bound by the passes' latency (four, one
-// cluster barrier each).  8 units of 128K rows: 20 of the call's 34 us (clusters of
-// 16: 19).
-constexpr int kCmpThreads = 512;
-constexpr int kCmpKeys = 49152;  // keys held per CTA (192 KB)
+// match of equal buckets first took four times as long).  A warp's keys above tau
+// are counted in its histograms.  The weights are read once, sixteen a thread in
+// flight; bound by the passes' latency (four, one cluster barrier each, 2 us a
+// pass of few keys) and, with 16K keys a CTA, by the instructions over them.  8
+// units of 128K rows: 19 of the call's 31 us, 64 units of 8K rows: 12 of 21.
+// CTAs of more keys than this have 1024 threads where at most half of the SMs get
+// one, the others 512 (8 units of 128K rows, 64 CTAs of 16K keys: 31 against 34
+// us; 32 units of 70K, 128 CTAs of 17K: 52 against 30, clusters wait for one
+// another's SMs, and the copy, which waits beside the selection, for room).
+constexpr int kCmpMany = 8192;
+constexpr int kCmpKeys = 45056;  // keys held per CTA (176 KB)
 
 struct CompressParams {
   const float* weights;        // [U, S]
@@ -184,7 +189,7 @@ struct Keys4 {
   uint32_t k[4];
 };
 
-template <int CS>
+template <int CS, int kCmpThreads>
 __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const CompressParams p) {
   if (CS > 1) cluster_arrive_relaxed();
   pdl_next();  // the copy
@@ -271,6 +276,7 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
   // keys > tau are taken, and the first `need` keys equal to tau
   uint32_t prefix = 0u, mask = 0u;
   unsigned int need = static_cast<unsigned int>(p.budget);
+  unsigned int c_gt = 0u, c_eq = 0u;  // this warp's keys above tau and at tau
   for (int shift = 24; shift >= 0; shift -= 8) {
     unsigned int* mine = hc[(shift >> 3) & 1];
     for (int d = lane; d < 256; d += 32) hw[warp][d] = 0u;
@@ -343,20 +349,16 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
     prefix |= pick_sh[0] << shift;
     mask |= 255u << shift;
     need -= pick_sh[1];
+    // this warp's keys above the bucket, and in it, from its own histogram
+    const unsigned int sel = pick_sh[0];
+    unsigned int over = 0u;
+#pragma unroll
+    for (int d = lane; d < 256; d += 32) over += static_cast<unsigned int>(d) > sel ? hw[warp][d] : 0u;
+    c_gt += __reduce_add_sync(0xffffffffu, over);
+    c_eq = hw[warp][sel];
+    __syncwarp();  // read before it is cleared for the next pass
   }
   const uint32_t tau = prefix;
-  // keys above tau and at tau: of each warp, then of each CTA
-  unsigned int c_gt = 0, c_eq = 0;
-  for (int j = s0 + 4 * lane; j < s1; j += 128) {
-    const Keys4 k = keys_at(j);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c_gt += k.k[i] > tau;
-      c_eq += k.k[i] == tau && k.k[i] != 0u;
-    }
-  }
-  c_gt = __reduce_add_sync(0xffffffffu, c_gt);
-  c_eq = __reduce_add_sync(0xffffffffu, c_eq);
   if (lane == 0) {
     warp_part[0][warp] = c_gt;
     warp_part[1][warp] = c_eq;
@@ -384,54 +386,56 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
       eq += part[1][r];
     }
   }
-  // Row j goes behind the keys above tau and the kept ties before it.  A lane
-  // has four rows; those of the lanes below come from a scan of the counts.
+  // Row j goes behind the keys above tau and the kept ties before it: those of
+  // the lanes below, which have four rows each, by a vote for each of the four.
+  const unsigned int lower = (1u << lane) - 1u;
   for (int j0 = s0; j0 < s1; j0 += 128) {
     const int j = j0 + 4 * lane;
     Keys4 k{};
     if (j < s1) k = keys_at(j);
-    unsigned int mine = 0;  // above tau in the low half, at tau in the high one
+    unsigned int g = gt, all = 0u, ties = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      mine += (k.k[i] > tau ? 1u : 0u) + (k.k[i] == tau && k.k[i] != 0u ? 65536u : 0u);
-    unsigned int sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
+    for (int i = 0; i < 4; ++i) {
+      const unsigned int v = __ballot_sync(0xffffffffu, k.k[i] > tau);
+      g += __popc(v & lower);
+      all += __popc(v);
+      ties |= k.k[i] == tau && k.k[i] != 0u ? 1u << i : 0u;
     }
-    const unsigned int all = __shfl_sync(0xffffffffu, sum, 31);
-    unsigned int g = gt + ((sum - mine) & 0xffffu), q = eq + ((sum - mine) >> 16);
-    if (all >> 16 == 0u) {  // no ties among the warp's: few lanes have any
-      unsigned int bits = 0u;
+    if (!__any_sync(0xffffffffu, ties != 0u)) {
+      unsigned int to = g + min(eq, need);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bits |= (k.k[i] > tau ? 1u : 0u) << i;
-      unsigned int to = g + min(q, need);
-      while (bits != 0u) {
-        if (to < static_cast<unsigned int>(p.budget)) out[to] = lo + j + __ffs(bits) - 1;
-        bits &= bits - 1u;
-        ++to;
-      }
-    } else if (mine != 0u) {
+      for (int i = 0; i < 4; ++i)
+        if (k.k[i] > tau) {
+          if (to < static_cast<unsigned int>(p.budget)) out[to] = lo + j + i;
+          ++to;
+        }
+    } else {
+      unsigned int q = eq;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool above = k.k[i] > tau, tie = k.k[i] == tau && k.k[i] != 0u;
+        const unsigned int v = __ballot_sync(0xffffffffu, ties >> i & 1u);
+        q += __popc(v & lower);
+        eq += __popc(v);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool above = k.k[i] > tau, tie = ties >> i & 1u;
         const unsigned int to = g + min(q, need);
         if ((above || (tie && q < need)) && to < static_cast<unsigned int>(p.budget)) out[to] = lo + j + i;
         g += above;
         q += tie;
       }
     }
-    gt += all & 0xffffu;
-    eq += all >> 16;
+    gt += all;
   }
 }
 
+// ---------------------------------------------------------------- copy
 // Copy: destination slot i of unit u gets source row rows[u, i] (K, V, the
 // weight), and rows[u, i] becomes the row's position.  Bound by HBM: a warp
 // takes kCopyRows rows, half of its lanes the K rows and half the V rows,
 // every load of the warp in flight before its first store.  8 units of 8K rows
-// of D = 128 in bf16 (67 MB read and written): 14 of the call's 34 us, 75% of the
+// of D = 128 in bf16 (67 MB read and written): 12 of the call's 31 us, 88% of the
 // copy rate.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyRows = 4;
@@ -501,9 +505,9 @@ __global__ void __launch_bounds__(kCopyThreads) compress_copy_kernel(const CopyP
   }
 }
 
-template <int CS>
-cudaError_t launch_compress_select(const Launch& l, const CompressParams& p, int U, size_t smem) {
-  const void* fn = reinterpret_cast<const void*>(compress_select_kernel<CS>);
+template <int CS, int kCmpThreads>
+cudaError_t launch_select_threads(const Launch& l, const CompressParams& p, int U, size_t smem) {
+  const void* fn = reinterpret_cast<const void*>(compress_select_kernel<CS, kCmpThreads>);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -519,7 +523,15 @@ cudaError_t launch_compress_select(const Launch& l, const CompressParams& p, int
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, compress_select_kernel<CS>, p);
+  return cudaLaunchKernelEx(&cfg, compress_select_kernel<CS, kCmpThreads>, p);
+}
+
+template <int CS>
+cudaError_t launch_compress_select(const Launch& l, const CompressParams& p, int U, size_t smem) {
+  if constexpr (CS == 8)  // smaller clusters are for more units
+    if ((p.S + CS - 1) / CS > kCmpMany && 2 * U * CS <= l.num_sms)
+      return launch_select_threads<CS, 1024>(l, p, U, smem);
+  return launch_select_threads<CS, 512>(l, p, U, smem);
 }
 
 // Rows of `st`-strided tensors at `ptr` all start on a 16-byte boundary.

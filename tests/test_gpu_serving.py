@@ -266,6 +266,12 @@ def test_cache_compress(steps, csa, dtype, B, Hkv, Sn, T, D, n_sink, n_local, ti
         _same(dst, want)
 
 
+@pytest.mark.parametrize("B,Hkv,Sn,T,ties", [(1, 1, 65541, 65541, True), (2, 2, 70001, 300, True), (1, 3, 131072, 40000, False)])
+def test_cache_compress_many_rows(steps, csa, B, Hkv, Sn, T, ties):
+    """Few units of many rows: clusters of eight CTAs with more threads each."""
+    test_cache_compress(steps, csa, "bf16", B, Hkv, Sn, T, 64, 4, 10, ties)
+
+
 def test_cache_compress_keys_beyond_shared_memory(steps, csa):
     """More rows than eight CTAs hold keys for: they are read again each pass."""
     Sn, T = 8 * 49152 + 5, 64
