@@ -314,6 +314,8 @@ __global__ void __launch_bounds__(kF32Workers* kF32Threads) attend_f32_kernel(co
 constexpr int kMergeThreads = 256;
 constexpr int kMergeMinKeys = 1024;  // own keys per share at least
 constexpr int kMaxG = 16;
+constexpr int kMergeKept = 128;  // partials of a head whose weights are kept in shared memory
+constexpr int kMergeAhead = 4;   // heads whose logits are fetched ahead
 
 // Partials of one query head: `np` of its prefix unit, then `no` of its own
 // unit.  Prefix partial i lies at row (i >> psh) * pstep + (i & psh) * phalf
@@ -348,7 +350,23 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
   __shared__ float lse2[kMaxG];
   __shared__ MergeSrc src[kMaxG];
   __shared__ float4 red[kMergeThreads];
+  __shared__ float part_w[kMaxG][kMergeKept];  // exp(lse - L) of the partials, -1: not written
+  __shared__ float4 ahead[kMergeAhead][kMergeThreads];
+  // the first four keys' sums and logits of this thread come while the partials
+  // are looked up
+  float* acc = p.acc ? p.acc + static_cast<int64_t>(u) * s.T : nullptr;
+  const float* lg = p.logits + static_cast<int64_t>(u) * s.G * p.Tl;
+  const int64_t k1 = min(k0 + share, static_cast<int64_t>(len)), j_first = k0 + 4 * tid;
+  float old_first[4] = {0.f, 0.f, 0.f, 0.f};
+  if (acc != nullptr && p.decay != 0.f)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (j_first + i < k1) old_first[i] = acc[j_first + i];
   pdl_wait();  // the attention kernel's partials
+  if (acc != nullptr && j_first < k1)
+    for (int g = 0; g < min(s.G, kMergeAhead); ++g)
+      copy16(smem_u32(&ahead[g][tid]), lg + g * p.Tl + j_first, true);
+  asm volatile("cp.async.commit_group;" ::: "memory");
   for (int g = warp; g < s.G; g += kMergeThreads / 32) {
     MergeSrc m{};
     const int W = p.b.plan.starts[s.N + s.B], P = p.b.plan.starts[s.N + s.B + 1];
@@ -367,7 +385,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
         r -= tile * R;
         const int rows = min(R, seqs * s.G - tile * R);
         const int ui = h * tiles + tile, x = x_pre + ui * (c + ln.s.lead) + ln.s.lead;
-        const int c0 = pd_worker_of(x, Wl, Pl), c1 = pd_worker_of(x + c - 1, Wl, Pl);
+        const PdCut cut(Wl, Pl);
+        const int c0 = cut.worker_of(x), c1 = cut.worker_of(x + c - 1);
         if (ln.halves == 2) {
           const int rh = R / 2;
           m.psh = rows <= rh ? 1 : 0;
@@ -384,7 +403,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
     const int c = pd_chunks(s, len);
     if (c > 0) {
       const int x = x_own + h * (c + s.lead) + s.lead;
-      const int c0 = pd_worker_of(x, W, P), c1 = pd_worker_of(x + c - 1, W, P);
+      const PdCut cut(W, P);
+      const int c0 = cut.worker_of(x), c1 = cut.worker_of(x + c - 1);
       m.no = c1 - c0 + 1;
       const int64_t row = (static_cast<int64_t>(c0) + u) * s.G + g;
       m.ostep = s.G;
@@ -411,6 +431,9 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float L = sum == 0.f ? -INFINITY : base + log2f(sum);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      part_w[g][lane + 32 * k] = lv[k] == -INFINITY ? -1.f : exp2f(lv[k] - L);
     if (lane == 0) {
       lse2[g] = L;
       src[g] = m;
@@ -418,6 +441,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
   }
   __syncthreads();
   if (tasks > 0) {
+    constexpr int kFly = 4;
     // few tasks: several threads each, over the partials
     const int parts = max(1, kMergeThreads / tasks);
     for (int t0 = 0; t0 < tasks; t0 += kMergeThreads) {
@@ -428,24 +452,28 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
         const MergeSrc m = src[g];
         const float L = lse2[g];
         const int ns = L == -INFINITY ? 0 : m.np + m.no;
-        for (int i = part; i < ns; i += 4 * parts) {  // four rows in flight
-          float w[4];
-          float4 v[4];
+        for (int i = part; i < ns; i += kFly * parts) {  // kFly rows in flight
+          float w[kFly];
+          float4 v[kFly];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < kFly; ++k) {
             const int j = min(i + k * parts, ns - 1);
-            w[k] = m.lse(j);
             v[k] = ld4(j < m.np ? m.po + m.prow(j) * D + d : m.oo + m.orow(j - m.np) * D + d);
+            if (j < kMergeKept) {
+              w[k] = part_w[g][j];
+            } else {
+              const float x = m.lse(j);
+              w[k] = x == -INFINITY ? -1.f : exp2f(x - L);
+            }
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // a row whose lse is -inf was not written
-            if (i + k * parts < ns && w[k] != -INFINITY) {
-              const float e = exp2f(w[k] - L);
-              o.x += e * v[k].x;
-              o.y += e * v[k].y;
-              o.z += e * v[k].z;
-              o.w += e * v[k].w;
+          for (int k = 0; k < kFly; ++k) {
+            // a row whose lse is -inf was not written (a NaN is one that was)
+            if (i + k * parts < ns && !(w[k] < 0.f)) {
+              o.x += w[k] * v[k].x;
+              o.y += w[k] * v[k].y;
+              o.z += w[k] * v[k].z;
+              o.w += w[k] * v[k].w;
             }
           }
         }
@@ -484,21 +512,23 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
   }
   if (blockIdx.x == 0 && p.lse_out && tid < s.G)
     p.lse_out[static_cast<int64_t>(b) * p.Hq + h * s.G + tid] = lse2[tid] * kPdLn2;
-  if (p.acc != nullptr) {
-    float* acc = p.acc + static_cast<int64_t>(u) * s.T;
-    const float* lg = p.logits + static_cast<int64_t>(u) * s.G * p.Tl;
-    const int64_t k1 = min(k0 + share, static_cast<int64_t>(len));
+  if (acc != nullptr) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // each thread reads its own only
     // four keys a thread, four heads' logits in flight: their rows start on 16
     // bytes, the sums' need not
-    for (int64_t j = k0 + 4 * tid; j < k1; j += 4 * kMergeThreads) {
+    for (int64_t j = j_first; j < k1; j += 4 * kMergeThreads) {
+      const bool first = j == j_first;
       float w[4] = {0.f, 0.f, 0.f, 0.f}, old[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) old[i] = p.decay != 0.f && j + i < k1 ? acc[j + i] : 0.f;
+      for (int i = 0; i < 4; ++i)
+        old[i] = first ? old_first[i] : p.decay != 0.f && j + i < k1 ? acc[j + i] : 0.f;
       for (int g0 = 0; g0 < s.G; g0 += 4) {
         float4 x[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          if (g0 + g < s.G) x[g] = ld4(lg + (g0 + g) * p.Tl + j);
+          if (g0 + g < s.G)
+            x[g] = first && g0 + g < kMergeAhead ? ahead[(g0 + g) % kMergeAhead][tid]
+                                                 : ld4(lg + (g0 + g) * p.Tl + j);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const float L = g0 + g < s.G ? lse2[g0 + g] : -INFINITY;

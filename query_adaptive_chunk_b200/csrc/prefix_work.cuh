@@ -161,11 +161,27 @@ __device__ __forceinline__ uint64_t pd_scan(uint64_t v, uint64_t* sh, int warps,
   return before + x - v;
 }
 
-// Places of W before worker c of P (c <= P <= 2^15).
-__device__ __forceinline__ int pd_cut(int W, int c, int P) {
-  const int q = W / P;
-  return q * c + (W - q * P) * c / P;
-}
+// W places over P < 2^11 workers, P <= W < 2^31.
+struct PdCut {
+  int P, q, r;  // W = q P + r
+  float inv_P, per_place;
+  __device__ __forceinline__ PdCut(int W, int workers) : P(workers), q(W / workers) {
+    r = W - q * P;
+    inv_P = __frcp_rn(static_cast<float>(P));
+    per_place = static_cast<float>(P) / static_cast<float>(W);
+  }
+  // Places before worker c <= P: floor(W c / P).  r c < 2^22 is exact, and (r c +
+  // 1/2) / P lies 1 / 2P = 2^-12 or more from the integers, its error (two
+  // roundings of 2^-24 of less than 2^11) below that.
+  __device__ __forceinline__ int before(int c) const {
+    return q * c + static_cast<int>((static_cast<float>(r * c) + 0.5f) * inv_P);
+  }
+  // The worker that holds place x: (x + 1/2) P / W is within one of it.
+  __device__ __forceinline__ int worker_of(int x) const {
+    const int c = min(P - 1, static_cast<int>((static_cast<float>(x) + 0.5f) * per_place));
+    return before(c) > x ? c - 1 : before(c + 1) <= x ? c + 1 : c;
+  }
+};
 
 // What a CTA works on.
 struct PdPlace {
@@ -239,7 +255,8 @@ __device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b,
     // lane k: worker k's bounds
     const int wk = min(lane, nw);
     const int c_lane = me.spread ? wk * b.ctas + block : block * nw + wk;
-    const int x_lane = pd_cut(W, min(P, c_lane), P), xe_lane = pd_cut(W, min(P, c_lane + 1), P);
+    const PdCut cut(max(1, W), P);
+    const int x_lane = cut.before(min(P, c_lane)), xe_lane = cut.before(min(P, c_lane + 1));
     // this warp's 32 items, from item i0 on: lane k looks worker k's first place up
     // among them (the last item that starts at or before it)
     auto place = [&](int i0, int n_keys, uint64_t at, uint64_t mine) {
@@ -389,11 +406,5 @@ struct PdWalk {
     return false;
   }
 };
-
-// The worker of P that holds place x of W: (x + 1) P - 1 < 2^46 is exact in
-// 64-bit floats, and the quotient is at least 2^-31 away from the next integer.
-__device__ __forceinline__ int pd_worker_of(int x, int W, int P) {
-  return static_cast<int>((static_cast<double>(x + 1) * P - 1.0) / W);
-}
 
 }  // namespace csa
