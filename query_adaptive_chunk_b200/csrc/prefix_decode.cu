@@ -369,15 +369,26 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
   asm volatile("cp.async.commit_group;" ::: "memory");
   for (int g = warp; g < s.G; g += kMergeThreads / 32) {
     MergeSrc m{};
-    const int W = p.b.plan.starts[s.N + s.B], P = p.b.plan.starts[s.N + s.B + 1];
-    const int x_own = p.b.plan.starts[s.N + b];
-    const int n = s.N > 0 ? p.b.plan.group[b] : -1;
+    // one round of loads: both lines' plans, and with one prefix its entries
+    // whether the sequence has it or not
+    const int items = s.N + s.B;
+    const int32_t* sb = p.b.plan.starts;
+    const int W = sb[items], P = sb[items + 1];
+    const int x_own = sb[s.N + b];
+    const int n = s.N == 0 ? -1 : s.N == 1 ? 0 : p.b.plan.group[b];
     if (n >= 0) {
-      const int g0 = p.b.plan.gsan[n], seqs = p.b.plan.gsan[n + 1] - g0;
-      const PdLine& ln = p.a.s.ctas > 0 && seqs * s.G >= p.a.s.min_rows ? p.a : p.b;
-      const int x_pre = ln.plan.starts[n], ub = ln.plan.ubase[n];
-      const int Wl = ln.plan.starts[s.N + s.B], Pl = ln.plan.starts[s.N + s.B + 1];
-      const int c = pd_chunks(ln.s, pd_prefix_len(s, n));
+      const bool two = p.a.s.ctas > 0;
+      const int32_t* sa = two ? p.a.plan.starts : sb;
+      const int g0 = p.b.plan.gsan[n], g1 = p.b.plan.gsan[n + 1], seqs = g1 - g0;
+      const int xa = sa[n], Wa = sa[items], Pa = sa[items + 1];
+      const int ua = (two ? p.a.plan.ubase : p.b.plan.ubase)[n];
+      const int xb = sb[n], unb = p.b.plan.ubase[n];
+      const int keys = pd_prefix_len(s, n);
+      const bool on_a = two && seqs * s.G >= p.a.s.min_rows;
+      const PdLine& ln = on_a ? p.a : p.b;
+      const int x_pre = on_a ? xa : xb, ub = on_a ? ua : unb;
+      const int Wl = on_a ? Wa : W, Pl = on_a ? Pa : P;
+      const int c = g0 <= b && b < g1 ? pd_chunks(ln.s, keys) : 0;
       if (c > 0) {
         const int tiles = pd_tiles(ln.s, seqs), R = ln.s.R;
         int r = (b - g0) * s.G + g;
