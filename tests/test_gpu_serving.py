@@ -455,6 +455,27 @@ def test_decode_refuses(csa, steps):
         steps.SharedPrefixDecoder(steps.TokenCache(odd, odd), Hq=8).attend(q)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_steps_back_to_back(steps, dtype):
+    """Steps in a row, with and without waiting between them: a step's merge
+    reads the sums ahead of its attention, but not ahead of the step before."""
+    B, Hkv, G, D, T, Tp = 7, 2, 4, 64, 90, 700
+    q, K, V, Kp, Vp = _decode_case(dtype, B, Hkv, G, D, 1, Tp, T, [Tp], [0, 5], [T] * B, 8, poison=False)
+    k, v = K[:, :, 0].contiguous(), V[:, :, 1].contiguous()
+    outs = []
+    for wait in (True, False):
+        cache = steps.TokenCache(K.clone(), V.clone(), lengths=torch.full((B,), T - 3, dtype=torch.int32, device="cuda"),
+                                 next_pos=torch.full((B,), T - 3, dtype=torch.int32, device="cuda"), budget=T - 1)
+        dec = steps.SharedPrefixDecoder(cache, Hq=Hkv * G, Kp=Kp, Vp=Vp, decay=0.9,
+                                        group_start=torch.tensor([0, 5], dtype=torch.int32, device="cuda"))
+        for _ in range(60):
+            out, lse = dec.step(q, k, v)
+            if wait:
+                torch.cuda.synchronize()
+        outs.append((out.clone(), lse.clone(), cache.weights.clone(), cache.positions.clone(), cache.K.clone()))
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
 def test_decode_is_deterministic(steps):
     """No sum depends on the order in which SMs finish."""
     q, K, V, Kp, Vp = _decode_case("bf16", 9, 2, 4, 128, 1, 3000, 300, [3000], [0, 9], [300] * 9, 4, poison=False)
