@@ -78,6 +78,13 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
     if (at >= 0 && n >= 0 && n <= c.budget) arrived = atomicAdd(c.counters + b, 1);
   }
   load(tid);  // most often the cache is full: its slots' loads go out beside the length's
+  // and so do the new row's: K by the first 64 threads, V by the next, 16 bytes each
+  const int es = c.bf16 ? 2 : 4, bytes = c.D * es;
+  const bool is_v = tid >= 64, ahead = wide && bytes <= 1024;
+  const char* from = is_v ? v + (b * vb + h * vh) * es : k + (b * kb + h * kh) * es;
+  const int off = (tid & 63) * 16;
+  uint4 row = make_uint4(0u, 0u, 0u, 0u);
+  if (ahead && tid < 128 && off < bytes) row = *reinterpret_cast<const uint4*>(from + off);
   __syncthreads();
   const int len = sh_len, next = sh_next;
   if (next < 0) return;  // an inactive sequence: left alone
@@ -116,14 +123,14 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
     slot = best == ~0ull ? -1 : static_cast<int>(best & 0xffffffffu);
   }
   if (slot >= 0) {
-    const int es = c.bf16 ? 2 : 4;
-    char* K = static_cast<char*>(c.K) + (b * c.kst[0] + h * c.kst[1] + slot * c.kst[2]) * es;
-    char* V = static_cast<char*>(c.V) + (b * c.vst[0] + h * c.vst[1] + slot * c.vst[2]) * es;
-    if (tid < 64)
-      copy_row(K, k + (b * kb + h * kh) * es, c.D * es, wide, tid, 64);
-    else if (tid < 128)
-      copy_row(V, v + (b * vb + h * vh) * es, c.D * es, wide, tid - 64, 64);
-    else if (tid == 128)
+    if (tid < 128) {
+      char* to = is_v ? static_cast<char*>(c.V) + (b * c.vst[0] + h * c.vst[1] + slot * c.vst[2]) * es
+                      : static_cast<char*>(c.K) + (b * c.kst[0] + h * c.kst[1] + slot * c.kst[2]) * es;
+      if (!ahead)
+        copy_row(to, from, bytes, wide, tid & 63, 64);
+      else if (off < bytes)
+        *reinterpret_cast<uint4*>(to + off) = row;
+    } else if (tid == 128)
       c.weights[static_cast<int64_t>(u) * c.T + slot] = 0.f;
     else if (tid == 160)
       c.positions[static_cast<int64_t>(u) * c.T + slot] = next;
