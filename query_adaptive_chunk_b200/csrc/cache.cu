@@ -45,8 +45,8 @@ __device__ __forceinline__ void copy_row(void* dst, const void* src, int bytes, 
 // the first warps write the new row.  The sequence's length and next position are shared
 // by its heads: each CTA reads them before it arrives at the sequence's
 // counter, and the last one to arrive advances them and clears the counter.
-// 4 sequences of 4 heads and 257 slots: 3.8 us; 64 of 8 heads and 4096 slots
-// (17 MB, 2.7 us at the copy rate): 7.5 us.
+// 4 sequences of 4 heads and 257 slots: 3.6 us; 64 of 8 heads and 4096 slots
+// (17 MB, 2.7 us at the copy rate): 7.3 us.
 constexpr int kInsThreads = 512;
 
 __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
@@ -160,10 +160,10 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
 // flight; bound by the passes' latency (four, one cluster barrier each, 2 us a
 // pass of few keys) and, with 16K keys a CTA, by the instructions over them.  8
 // units of 128K rows: 19 of the call's 31 us, 64 units of 8K rows: 12 of 21.
-// CTAs of more keys than this have 1024 threads where at most half of the SMs get
-// one, the others 512 (8 units of 128K rows, 64 CTAs of 16K keys: 31 against 34
-// us; 32 units of 70K, 128 CTAs of 17K: 52 against 30, clusters wait for one
-// another's SMs, and the copy, which waits beside the selection, for room).
+// CTAs of more keys than this have 1024 threads where each has an SM, the others
+// 512 (8 units of 128K rows, 64 CTAs of 16K keys: 31 against 34 us; 128 units of
+// 20K, a CTA each: 29 against 31; 32 units of 70K as 256 CTAs: 52 against 30, the
+// second half waits for the first).
 constexpr int kCmpMany = 8192;
 constexpr int kCmpKeys = 45056;  // keys held per CTA (176 KB)
 
@@ -535,9 +535,8 @@ cudaError_t launch_select_threads(const Launch& l, const CompressParams& p, int 
 
 template <int CS>
 cudaError_t launch_compress_select(const Launch& l, const CompressParams& p, int U, size_t smem) {
-  if constexpr (CS == 8)  // smaller clusters are for more units
-    if ((p.S + CS - 1) / CS > kCmpMany && 2 * U * CS <= l.num_sms)
-      return launch_select_threads<CS, 1024>(l, p, U, smem);
+  if ((p.S + CS - 1) / CS > kCmpMany && U * CS <= l.num_sms)
+    return launch_select_threads<CS, 1024>(l, p, U, smem);
   return launch_select_threads<CS, 512>(l, p, U, smem);
 }
 
@@ -567,9 +566,10 @@ cudaError_t launch_cache_compress(const Launch& l, const CacheArgs& dst, const C
     CompressParams p{s.weights, s.positions,  s.len,       s.next_pos, s.S,           dst.Hkv,
                      dst.budget, dst.n_sink, dst.n_local, dst.T,      dst.positions, 0,
                      l.err};
-    // CTAs per unit: 2048 rows or more each, while all run at once (two per SM)
+    // CTAs per unit: 2048 rows or more each, while each has an SM (two per SM: 32
+    // units of 16K rows 19.0 against 16.8 us, 64 of 8K 21.8 against 20.9)
     int CS = 1;
-    while (CS < 8 && s.S > 2048ll * CS && U * CS <= l.num_sms) CS *= 2;
+    while (CS < 8 && s.S > 2048ll * CS && 2 * U * CS <= l.num_sms) CS *= 2;
     while (CS < 8 && (s.S + CS - 1) / CS > kCmpKeys) CS *= 2;
     const int64_t per = (s.S + CS - 1) / CS;
     p.held = per <= kCmpKeys ? 1 : 0;

@@ -266,10 +266,12 @@ def test_cache_compress(steps, csa, dtype, B, Hkv, Sn, T, D, n_sink, n_local, ti
         _same(dst, want)
 
 
-@pytest.mark.parametrize("B,Hkv,Sn,T,ties", [(1, 1, 65541, 65541, True), (2, 2, 70001, 300, True), (1, 3, 131072, 40000, False)])
+@pytest.mark.parametrize("B,Hkv,Sn,T,ties", [(1, 1, 65541, 65541, True), (2, 2, 70001, 300, True), (1, 3, 131072, 40000, False),
+                                              (4, 8, 40003, 100, True), (9, 8, 20001, 77, True), (10, 8, 9001, 50, False)])
 def test_cache_compress_many_rows(steps, csa, B, Hkv, Sn, T, ties):
-    """Few units of many rows: clusters of eight CTAs with more threads each."""
-    test_cache_compress(steps, csa, "bf16", B, Hkv, Sn, T, 64, 4, 10, ties)
+    """Many rows a unit: CTAs, alone and in clusters of two, four and eight, with
+    more threads each."""
+    test_cache_compress(steps, csa, "bf16", B, Hkv, Sn, T, 8, 4, 10, ties)
 
 
 def test_cache_compress_keys_beyond_shared_memory(steps, csa):
