@@ -18,8 +18,8 @@
 // angles are formed once per J heads' worth of threads; loads are up to 16
 // bytes, two heads in flight per thread (four leave too few threads: 173
 // against 120 us), the first ones under way while the angles are formed.  32K
-// tokens of 40 heads of 128 (bf16, a packed projection's views): 120 us, 5.6
-// TB/s, 87% of the copy rate.
+// tokens of 40 heads of 128 (bf16, a packed projection's views): 113 us, 5.9
+// TB/s, 92% of the copy rate.
 #include <algorithm>
 
 #include "internal.h"
@@ -84,10 +84,10 @@ __device__ __forceinline__ void st_vec(void* p, const VT& v) {
 // HALF: V pairs from two V-wide accesses rot/2 apart; otherwise V/2 pairs
 // from one V-wide access.
 constexpr int kRotFlight = 2;  // heads in flight per thread
-constexpr int kRotBlocks = 3;  // blocks per SM at least
 
-template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(kRotThreads, kRotBlocks) rotary_kernel(const RotParams p) {
+// BLOCKS: per SM at least.
+template <typename T, int V, bool HALF, int BLOCKS>
+__global__ void __launch_bounds__(kRotThreads, BLOCKS) rotary_kernel(const RotParams p) {
   constexpr int NP = HALF ? V : V / 2;
   constexpr int U = kRotFlight;
   using VT = Vec<T, V>;
@@ -215,18 +215,26 @@ __global__ void rotary_table_kernel(const TableParams p) {
   p.table[i] = f >= 0x1p64 ? 0ull : static_cast<uint64_t>(f);
 }
 
+template <typename T, int V, int BLOCKS>
+cudaError_t launch_blocks(const Launch& l, const RotParams& p, bool half, unsigned grid) {
+  if (half) {
+    rotary_kernel<T, V, true, BLOCKS><<<grid, kRotThreads, 0, l.stream>>>(p);
+  } else {
+    // a pair is two neighbours: the one-element width does not occur
+    if constexpr (V >= 2) rotary_kernel<T, V, false, BLOCKS><<<grid, kRotThreads, 0, l.stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+// Four blocks per SM keep more loads in flight over a long run, three spill
+// nothing, which counts in a short one (32K tokens of 40 heads 113 against 121
+// us, 8K tokens of 56 heads of 64, 3.4 blocks per SM in all, 32.6 against 30.6).
 template <typename T, int V>
 cudaError_t launch_v(const Launch& l, const RotParams& p, bool half) {
   const int64_t threads = static_cast<int64_t>(p.tokens) * p.J * (p.nrot + p.ntail);
-  const int64_t grid = (threads + kRotThreads - 1) / kRotThreads;
-  if (half) {
-    rotary_kernel<T, V, true><<<static_cast<unsigned>(grid), kRotThreads, 0, l.stream>>>(p);
-  } else {
-    // a pair is two neighbours: the one-element width does not occur
-    if constexpr (V >= 2)
-      rotary_kernel<T, V, false><<<static_cast<unsigned>(grid), kRotThreads, 0, l.stream>>>(p);
-  }
-  return cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>((threads + kRotThreads - 1) / kRotThreads);
+  return grid > 8u * l.num_sms ? launch_blocks<T, V, 4>(l, p, half, grid)
+                               : launch_blocks<T, V, 3>(l, p, half, grid);
 }
 
 template <typename T>
@@ -295,12 +303,14 @@ cudaError_t launch_rotary(const Launch& l, const RotaryArgs& a) {
   p.positions = a.positions;
   p.pos_b = a.pos_stride_b;
   p.pos0 = a.pos0;
-  // Heads side by side: four keep a warp's accesses in long runs; more when
-  // the tokens alone are too few to fill the SMs.
+  // Heads side by side: up to four keep a warp's accesses in long runs, but with
+  // eight heads a thread at least to share its angles (16K to 200K tokens of 2 to
+  // 6 heads: half the time that four side by side take); more when the tokens
+  // alone are too few to fill the SMs.
   const int64_t per_token = p.nrot + p.ntail;
   const int64_t want = 1024ll * l.num_sms;
   const int64_t lanes = p.tokens * per_token;
-  p.J = static_cast<uint32_t>(std::min<int64_t>(H, std::max<int64_t>(4, (want + lanes - 1) / lanes)));
+  p.J = static_cast<uint32_t>(std::min<int64_t>(H, std::max<int64_t>(std::max(1, std::min(4, H / 8)), (want + lanes - 1) / lanes)));
   return a.bf16 ? launch_t<__nv_bfloat16>(l, p, a.half, V) : launch_t<float>(l, p, a.half, V);
 }
 
