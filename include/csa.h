@@ -766,7 +766,9 @@ CSA_API csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_s
  *   weights[b, h, j] = decay weights[b, h, j] + sum_g exp(s_gj - lse_g) for the
  *          own slots j < len[b] (decay 0: the old value is not read)
  * A row with no key gets out = 0, lse = -inf.  K and V rows past the lengths
- * are never used, whatever they hold.
+ * are never used, whatever they hold.  A sequence whose next_pos is negative
+ * (inactive, as for csa_cache_insert) has no keys here, of its prefix or its own, and its
+ * weights stay as they are.
  *   q [B, Hq, D] dense;  out [B, Hq, D] of out_dtype;  lse_out NULL or [B, Hq]
  *   fp32;  weights NULL or [B, Hkv, T] fp32
  *   N prefixes (0: none): Kp, Vp [N, Hkv, Tp, D] by strides (prefix, head,
@@ -807,6 +809,7 @@ typedef struct csa_prefix_decode_desc {
   float decay;
   void* workspace;
   int64_t workspace_bytes;
+  const int32_t* next_pos; /* NULL (all active) or [B] */
 } csa_prefix_decode_desc;
 
 /* `weights`: whether the calls add up weights.  < 0 on sizes csa_prefix_decode

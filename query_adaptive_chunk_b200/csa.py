@@ -454,7 +454,7 @@ class PrefixDecodeDesc(ctypes.Structure):
         ("vp_stride", _st3), ("prefix_len", _vp), ("group_start", _vp), ("T", _i64), ("K", _vp),
         ("V", _vp), ("k_stride", _st3), ("v_stride", _st3), ("len", _vp), ("out", _vp),
         ("out_dtype", _i), ("lse_out", _vp), ("weights", _vp), ("decay", _f), ("workspace", _vp),
-        ("workspace_bytes", _i64),
+        ("workspace_bytes", _i64), ("next_pos", _vp),
     ]
 
 

@@ -1501,6 +1501,7 @@ csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream)
   CSA_TRY(check_ptr(d->prefix_len, "prefix_len", false));
   CSA_TRY(check_ptr(d->group_start, "group_start", false));
   CSA_TRY(check_ptr(d->len, "len", false));
+  CSA_TRY(check_ptr(d->next_pos, "next_pos", false));
   CSA_TRY(check_ptr(d->lse_out, "lse_out", false));
   CSA_TRY(check_ptr(d->weights, "weights", false));
   CSA_TRY(check_ptr(d->workspace, "workspace"));
@@ -1536,6 +1537,7 @@ csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream)
   a.prefix_len = d->prefix_len;
   a.group_start = d->group_start;
   a.len = d->len;
+  a.next_pos = d->next_pos;
   a.out = d->out;
   a.lse_out = d->lse_out;
   a.weights = d->weights;

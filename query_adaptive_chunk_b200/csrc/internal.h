@@ -175,7 +175,7 @@ struct PrefixDecodeArgs {
   const void *Kp, *Vp, *K, *V;
   int64_t kps[3], vps[3], ks[3], vs[3];     // strides: prefix / sequence, head, token
   int64_t Tp, T;
-  const int32_t *prefix_len, *group_start, *len;
+  const int32_t *prefix_len, *group_start, *len, *next_pos;
   void* out;
   float *lse_out, *weights;
   float decay;

@@ -480,7 +480,8 @@ class SharedPrefixDecoder:
     sequences group_start[n] .. group_start[n+1]-1 share prefix n (default: one
     prefix for all).  accumulate: add each step's attention weights on the own
     slots to cache.weights, the old sums times `decay` first.  rotary: turns
-    the queries and new keys of ``step`` at cache.next_pos."""
+    the queries and new keys of ``step`` at cache.next_pos.  An inactive sequence
+    (cache.next_pos negative) gets out = 0 and lse = -inf, and its sums stay."""
 
     def __init__(self, cache: TokenCache, *, Hq: int, Kp=None, Vp=None, prefix_len=None,
                  group_start=None, accumulate: bool = True, decay: float = 1.0,
@@ -514,7 +515,7 @@ class SharedPrefixDecoder:
             N=N, Tp=Tp, T=T, K=cache.K, V=cache.V, k_stride=cache.k_stride, v_stride=cache.v_stride,
             len=cache.lengths, out=self.out, out_dtype=out_dtype, lse_out=self.lse,
             weights=cache.weights if accumulate else None, decay=decay, workspace=self.workspace,
-            workspace_bytes=nbytes, **kw)
+            workspace_bytes=nbytes, next_pos=cache.next_pos, **kw)
 
     def attend(self, q: torch.Tensor, stream=None):
         """Attention of q [B, Hq, D] over the prefixes and the cache as they

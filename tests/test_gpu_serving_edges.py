@@ -1,0 +1,113 @@
+"""Serving operators on the GPU: states and calls that an ordinary batch does
+not have (paused sequences, positions at the end of their range, gradients
+through autograd, refused steps), against the fp64 oracle or the exact values."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as S
+from oracle.pipeline import to_np
+
+pytestmark = pytest.mark.gpu
+
+U32, U16 = 2.0 ** -24, 2.0 ** -8
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def csa():
+    from query_adaptive_chunk_b200 import csa as mod
+    return mod
+
+
+@pytest.fixture(scope="module")
+def steps():
+    from query_adaptive_chunk_b200 import steps as mod
+    return mod
+
+
+def _randn(shape, seed, dtype=torch.float32):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------- paused sequences
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,prefixes", [(4, 1), (4, 0), (12, 1), (2, 2)])
+def test_step_leaves_a_paused_sequence_alone(steps, csa, dtype, G, prefixes):
+    """A negative next position: no key enters, the sums stay as they are (whatever
+    the unused query and key rows hold), out = 0 and lse = -inf; the others
+    get what they get without it.  Unpaused, it goes on where it was."""
+    B, Hkv, D, T, Tp = 6, 2, 64, 70, 150
+    dt = DT[dtype]
+    Kp, Vp = _randn((max(1, prefixes), Hkv, Tp, D), 1, dt), _randn((max(1, prefixes), Hkv, Tp, D), 2, dt)
+    kw = {}
+    if prefixes:
+        kw = dict(Kp=Kp, Vp=Vp, group_start=_i32([0, 4] if prefixes == 1 else [0, 2, 5]))
+    K, V = _randn((B, Hkv, T, D), 3, dt), _randn((B, Hkv, T, D), 4, dt)
+    q, k, v = (_randn((B, n, D), 5 + n, dt) for n in (Hkv * G, Hkv, Hkv))
+    paused = [1, 5]
+
+    def run(pause):
+        cache = steps.TokenCache(K.clone(), V.clone(), lengths=_i32([T, 40, 0, 1, 69, T]), n_local=3,
+                                 next_pos=_i32([T, 40, 0, 1, 69, T]), positions=torch.arange(T, dtype=torch.int32, device="cuda").expand(B, Hkv, T).contiguous(),
+                                 weights=_randn((B, Hkv, T), 9).argsort(-1).float() + 1)  # far apart
+        before = {n: getattr(cache, n).clone() for n in ("K", "V", "weights", "positions", "lengths")}
+        dec = steps.SharedPrefixDecoder(cache, Hq=Hkv * G, decay=0.5, rotary=steps.Rotary(32), **kw)
+        held = cache.next_pos.clone()
+        qs, ks = q.clone(), k.clone()
+        if pause:
+            cache.next_pos[paused] = -7
+            qs[paused], ks[paused] = float("nan"), float("nan")
+        for _ in range(2):
+            out, lse = dec.step(qs, ks, v)
+            csa.csa_check_device_status()
+        got = out.clone(), lse.clone(), cache.weights.clone(), cache.K.clone(), cache.lengths.clone(), cache.positions.clone()
+        if not pause:
+            return got
+        assert cache.next_pos[paused].tolist() == [-7, -7]
+        for n, x in before.items():
+            assert torch.equal(getattr(cache, n)[paused], x[paused]), n
+        assert not out[paused].any() and bool((lse[paused] == -math.inf).all())
+        cache.next_pos[paused] = held[paused]
+        for _ in range(2):
+            out, lse = dec.step(q, k, v)
+        csa.csa_check_device_status()
+        return got, (out.clone(), lse.clone(), cache.weights.clone())
+
+    want = run(False)
+    got, later = run(True)
+    others = [b for b in range(B) if b not in paused]
+    # Without the paused sequences' keys the split of the others' is another, and so is the
+    # order of their sums: a logit and the running sums are good to 2^-20 + 2 * 68 * 2^-24
+    # sum |q k| / 8 < 1e-4 of a weight, an output to that and to bf16's rounding of the
+    # weights; two runs of two steps of G <= 12 weights each.
+    u = U16 if dtype == "bf16" else 0.0
+    vmax = float(max(V.abs().max(), v.abs().max(), Vp.abs().max()))
+    for rows, (o, l, w) in ((others, got[:3]), (paused, later)):
+        assert float((o[rows] - want[0][rows]).abs().max()) <= 2 * (1e-4 + u) * vmax
+        assert float((l[rows] - want[1][rows]).abs().max()) <= 2e-4
+        assert float((w[rows] - want[2][rows]).abs().max()) <= 2 * 2 * 12 * 1e-4
+    for x, y in zip(got[3:], want[3:]):
+        assert torch.equal(x[others], y[others])
+
+
+def test_attend_takes_a_paused_batch(steps, csa):
+    """Every sequence paused: nothing but zeros and -inf, the sums as they were."""
+    K = _randn((3, 2, 40, 128), 1, torch.bfloat16)
+    cache = steps.TokenCache(K, K.clone(), lengths=_i32([40, 3, 0]), next_pos=_i32([-1, -2, -(1 << 31)]),
+                             weights=_randn((3, 2, 40), 2))
+    before = cache.weights.clone()
+    Kp = _randn((1, 2, 300, 128), 3, torch.bfloat16)
+    dec = steps.SharedPrefixDecoder(cache, Hq=8, Kp=Kp, Vp=Kp, decay=0.0)
+    out, lse = dec.attend(_randn((3, 8, 128), 4, torch.bfloat16))
+    csa.csa_check_device_status()
+    assert not out.any() and bool((lse == -math.inf).all()) and torch.equal(cache.weights, before)
