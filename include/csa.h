@@ -735,7 +735,8 @@ CSA_API csa_status csa_cache_insert(const csa_cache_desc* c, const void* k,
  * `budget` (the lower row among equals; of more protected rows than fit, the
  * lowest), and copied in row order to slots 0 ..  with their weights and
  * positions; len[b] = the rows kept; c->next_pos (NULL: not written) = the
- * next position.
+ * next position.  Where that is negative (an inactive sequence) the last
+ * n_local count from the largest position among the (sequence, head)'s rows.
  *   src K, V by strides (sequence, head, row); weights [B, Hkv, S] fp32;
  *   positions NULL (the row number) or [B, Hkv, S] int32; src_next_pos NULL
  *   (n) or [B], required with positions.  n_sink + n_local <= budget.

@@ -122,9 +122,11 @@ def cache_compress(weights, lengths, budget, n_sink, n_local, positions=None, ne
     kept = []
     for b in range(B):
         n = int(lengths[b])
-        nxt = n if next_pos is None else int(next_pos[b])
         heads = []
         for h in range(Hkv):
+            nxt = n if next_pos is None else int(next_pos[b])
+            if nxt < 0:  # inactive: it stands behind its last row
+                nxt = n if positions is None else 1 + max((int(x) for x in positions[b, h, :n]), default=0)
             order = []
             for j in range(n):
                 at = j if positions is None else int(positions[b, h, j])

@@ -7,6 +7,7 @@
 // weight; NaN counts as -inf, equal weights go by the lower slot.  The rank
 // is taken on order-preserving 32-bit keys, so it is exact.
 #include <algorithm>
+#include <climits>
 
 #include "internal.h"
 
@@ -19,8 +20,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return w != w ? 0x007fffffu /* -inf's key */ : float_key(w);
 }
 
-__device__ __forceinline__ bool is_protected(int pos, int next, int n_sink, int n_local) {
-  return pos < n_sink || pos >= next - n_local;
+// `local`: the first of the last n_local positions.
+__device__ __forceinline__ bool is_protected(int pos, int n_sink, int local) {
+  return pos < n_sink || pos >= local;
 }
 
 // One row of `bytes` from src to dst by `n` threads (this one is `t`):
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int j = j0 + i * kInsThreads;
-        if (j < len && !is_protected(p[i], next, c.n_sink, c.n_local)) {
+        if (j < len && !is_protected(p[i], c.n_sink, next - c.n_local)) {
           const unsigned long long e =
               (static_cast<unsigned long long>(weight_key(x[i])) << 32) | static_cast<unsigned>(j);
           best = e < best ? e : best;
@@ -208,6 +210,7 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
   __shared__ unsigned int part[2][CS];      // keys above tau and at tau of each CTA
   __shared__ unsigned int warp_part[2][kWarps];
   __shared__ unsigned int pick_sh[2];
+  __shared__ int warp_last[kWarps], last[CS];  // largest positions (inactive sequences)
   const int rank = CS > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int u = blockIdx.x / CS, b = u / p.Hkv, tid = threadIdx.x, lane = tid & 31;
   const int warp = tid >> 5;
@@ -217,9 +220,6 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
   const int n = static_cast<int>(static_cast<int64_t>(len) * (rank + 1) / CS) - lo;
   const float* wrow = p.weights + static_cast<int64_t>(u) * p.S + lo;
   const int32_t* prow = p.positions ? p.positions + static_cast<int64_t>(u) * p.S + lo : nullptr;
-  auto make_key = [&](float w, int pos) -> uint32_t {
-    return is_protected(pos, next, p.n_sink, p.n_local) ? kKeyProtected : weight_key(w);
-  };
   const bool select = len > p.budget;
   int32_t* out = p.rows + static_cast<int64_t>(u) * p.T;
   if (CS > 1) cluster_wait();  // every CTA of the cluster is running
@@ -227,6 +227,34 @@ __global__ void __launch_bounds__(kCmpThreads) compress_select_kernel(const Comp
     for (int j = tid; j < n; j += kCmpThreads) out[lo + j] = lo + j;
     return;
   }
+  // An inactive sequence does not say where it stands: right behind its last row's
+  // position (the same branch for the whole cluster).
+  int64_t behind = next;
+  if (next < 0) {
+    if (prow == nullptr) {
+      behind = len;
+    } else {
+      int most = INT_MIN;
+      for (int j = tid; j < n; j += kCmpThreads) most = max(most, prow[j]);
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) warp_last[warp] = most;
+      __syncthreads();
+      for (int w = 0; w < kWarps; ++w) most = max(most, warp_last[w]);
+      if (CS > 1) {
+        if (tid < CS)
+          st_cluster_u32(cluster_map(smem_u32(&last[rank]), tid), static_cast<uint32_t>(most));
+        cluster_arrive();
+        cluster_wait();
+        for (int r = 0; r < CS; ++r) most = max(most, last[r]);
+      }
+      behind = static_cast<int64_t>(most) + 1;
+    }
+  }
+  const int local = static_cast<int>(
+      min(static_cast<int64_t>(INT_MAX), max(static_cast<int64_t>(INT_MIN), behind - p.n_local)));
+  auto make_key = [&](float w, int pos) -> uint32_t {
+    return is_protected(pos, p.n_sink, local) ? kKeyProtected : weight_key(w);
+  };
   const bool held = p.held != 0;
   if (held) {
     constexpr int U = 16;  // loads in flight

@@ -457,7 +457,7 @@ class TokenCache:
         S] (a prompt's, as csa_token_importance gives them, or another cache's):
         all rows below `lengths`, or the protected and the heaviest ones up to
         the budget, in row order.  positions [B, Hkv, S] with next_pos [B], else
-        the row numbers."""
+        the row numbers.  A sequence with a negative next_pos stays inactive."""
         B, Hkv, S, D = K.shape
         if (B, Hkv, D) != (self.B, self.Hkv, self.D):
             _bad("source K has other sizes than the cache")

@@ -111,3 +111,36 @@ def test_attend_takes_a_paused_batch(steps, csa):
     out, lse = dec.attend(_randn((3, 8, 128), 4, torch.bfloat16))
     csa.csa_check_device_status()
     assert not out.any() and bool((lse == -math.inf).all()) and torch.equal(cache.weights, before)
+
+
+@pytest.mark.parametrize("B,Hkv,Sn,T,n_sink,n_local", [
+    (3, 2, 100, 33, 4, 8), (2, 1, 4097, 1000, 4, 100), (1, 2, 20000, 513, 0, 300), (20, 8, 9000, 31, 2, 29),
+    (3, 1, 70001, 300, 8, 292), (2, 1, 400003, 64, 3, 17), (2, 2, 50, 20, 0, 0)])
+def test_compress_of_paused_sequences(steps, csa, B, Hkv, Sn, T, n_sink, n_local):
+    """A paused sequence's cache is compressed as another's: its sinks, the rows of its last
+    positions and the heaviest others stay, and so does the pause."""
+    rng = np.random.default_rng(Sn)
+    D = 6
+    w = rng.random((B, Hkv, Sn)).astype(np.float32)
+    pos = np.argsort(rng.random((B, Hkv, Sn)), -1) * 2 + 1
+    n = rng.integers(Sn // 2, Sn + 1, B)
+    n[0] = Sn
+    nxt = np.full(B, 2 * Sn + 5)
+    nxt[::2] = [-1 - (b * (1 << 31) // (2 * B)) for b in range(0, B, 2)]
+    nxt[0] = -(1 << 31)
+    K = _randn((B, Hkv, Sn, D), 3)
+    for given in (False, True):
+        cache = steps.TokenCache(torch.zeros(B, Hkv, T, D, device="cuda"), torch.zeros(B, Hkv, T, D, device="cuda"),
+                                 n_sink=n_sink, n_local=n_local)
+        cache.compress(K, K, torch.tensor(w, device="cuda"), lengths=_i32(n.tolist()), next_pos=_i32(nxt.tolist()),
+                       positions=_i32(pos.tolist()) if given else None)
+        csa.csa_check_device_status()
+        kept = S.cache_compress(w, n, T, n_sink, n_local, pos if given else None, nxt)
+        assert cache.next_pos.tolist() == nxt.tolist()
+        for b in range(B):
+            for h in range(Hkv):
+                rows = kept[b][h]
+                assert cache.lengths[b] == len(rows)
+                want = pos[b, h, rows] if given else rows
+                assert cache.positions[b, h, :len(rows)].tolist() == list(want)
+                assert torch.equal(cache.K[b, h, :len(rows)], K[b, h, rows])
