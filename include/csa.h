@@ -690,8 +690,9 @@ CSA_API csa_status csa_rotary(const csa_rotary_desc* d, csa_stream stream);
  * does not depend on it (keys are rotated already), and `positions` says
  * where each slot's token stands.
  *   K, V       [B, Hkv, T, D] of `dtype` by strides in elements (sequence,
- *              head, slot; last index dense; slots must not overlap; these and
- *              the rows copied into them need only their element's alignment)
+ *              head, slot; last index dense; slots that overlap, in K, in V or
+ *              between them, are refused; these and the rows copied into them need
+ *              only their element's alignment)
  *   weights    [B, Hkv, T] fp32, positions [B, Hkv, T] int32 (dense)
  *   len        [B] int32: slots in use, 0 .. budget; slots behind stay as they are
  *   next_pos   [B] int32: the next token's position; < 0: the sequence is
@@ -724,6 +725,7 @@ typedef struct csa_cache_desc {
  * one.  Needs n_sink + n_local < budget.  A length outside [0, budget], or no
  * unprotected slot (positions that are not distinct), records
  * CSA_ERR_DEVICE_INDEX and leaves that sequence's (that head's) slots alone.
+ * k and v must not overlap K or V (refused).
  * Calls that share a cache or its counters must not overlap on the GPU. */
 CSA_API csa_status csa_cache_insert(const csa_cache_desc* c, const void* k,
                                     const int64_t* k_stride, const void* v,

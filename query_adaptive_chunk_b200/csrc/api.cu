@@ -10,6 +10,7 @@
 
 #include "../../include/csa.h"
 #include "internal.h"
+#include "rows.h"
 
 // Device status word: [0] = first error code recorded by a kernel.
 __device__ int g_csa_status[4];
@@ -1259,6 +1260,24 @@ csa_status cache_ptrs(const csa_cache_desc* c, bool insert, Extent* ek, Extent* 
   return CSA_OK;
 }
 
+// The slots of the cache's K (is_v = false) or V.
+csa::Rows cache_rows(const csa_cache_desc* c, bool is_v) {
+  const int64_t* st = is_v ? c->v_stride : c->k_stride;
+  return csa::Rows{is_v ? c->V : c->K, 3, {c->B, c->Hkv, c->T}, {st[0], st[1], st[2]}, c->D,
+                   dtype_size(c->dtype)};
+}
+
+// A write to one slot must not be one to another: units are written side by side.
+csa_status cache_slots_apart(const csa_cache_desc* c) {
+  const csa::Rows K = cache_rows(c, false), V = cache_rows(c, true);
+  if (c->K == nullptr || c->V == nullptr) return CSA_OK;  // refused as pointers
+  for (int i = 0; i < 3; ++i)
+    CSA_REQUIRE(K.st[i] >= 0 && V.st[i] >= 0, "K / V: strides must be non-negative");
+  CSA_REQUIRE(!csa::rows_meet_themselves(K) && !csa::rows_meet_themselves(V), "K / V: rows overlap");
+  CSA_REQUIRE(!csa::rows_meet(K, V), "K and V overlap");
+  return CSA_OK;
+}
+
 csa::CacheArgs cache_args(const csa_cache_desc* c) {
   csa::CacheArgs a{};
   a.K = c->K;
@@ -1387,12 +1406,22 @@ csa_status csa_cache_insert(const csa_cache_desc* c, const void* k, const int64_
   CSA_TRY(cache_checks(c, true));
   CSA_REQUIRE(k_stride != nullptr && v_stride != nullptr, "k_stride / v_stride is NULL");
   if (c->B == 0) return CSA_OK;
+  CSA_TRY(cache_slots_apart(c));
+  const int es = dtype_size(c->dtype);
+  const int64_t n[2] = {c->B, c->Hkv};
+  for (int i = 0; i < 2; ++i)  // (units run side by side: one may write what another has yet to read)
+    for (int is_v = 0; is_v < 2; ++is_v) {
+      const void* p = i ? v : k;
+      const int64_t* st = i ? v_stride : k_stride;
+      if (p == nullptr || st[0] < 0 || st[1] < 0) continue;  // refused below
+      CSA_REQUIRE(!csa::rows_meet(csa::Rows{p, 2, {n[0], n[1], 0}, {st[0], st[1], 0}, c->D, es},
+                                  cache_rows(c, is_v)),
+                  "k / v and the cache overlap");
+    }
   Extent ek, ev, e1, e2;
   CSA_TRY(cache_ptrs(c, true, &ek, &ev));
-  const int es = dtype_size(c->dtype);
   CSA_TRY(check_ptr(k, "k", true, es));
   CSA_TRY(check_ptr(v, "v", true, es));
-  const int64_t n[2] = {c->B, c->Hkv};
   CSA_REQUIRE(extent_of(k, n, k_stride, 2, c->D, es, &e1) && extent_of(v, n, v_stride, 2, c->D, es, &e2),
               "k / v: strides must be non-negative");
   csa::Launch l;
@@ -1418,6 +1447,7 @@ csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* s
     CSA_REQUIRE(!x.overlaps(y), "the source's len must not be the cache's");
   }
   if (c->B == 0) return CSA_OK;
+  CSA_TRY(cache_slots_apart(c));
   Extent ek, ev, sk, sv;
   CSA_TRY(cache_ptrs(c, false, &ek, &ev));
   if (s->S > 0) {

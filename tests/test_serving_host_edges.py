@@ -29,3 +29,51 @@ def test_compress_of_a_paused_sequence_by_hand():
     assert S.cache_compress(w, [5], 3, 0, 2, pos, [-1]) == [[[0, 1, 3]]]
     assert S.cache_compress(w, [5], 3, 0, 2, pos, [10]) == [[[0, 1, 3]]]
     assert S.cache_compress(w, [5], 3, 0, 2, None, [-1]) == [[[1, 3, 4]]]
+
+
+def _cache(csa, **kw):
+    d = dict(dtype=1, B=2, Hkv=4, D=64, T=32, budget=32, K=1 << 20, V=1 << 30, k_stride=(8192, 2048, 64),
+             v_stride=(8192, 2048, 64))
+    d.update(kw)
+    return csa.cache_desc(**d)
+
+
+def _insert(csa, d, k, k_stride, v, v_stride):
+    two = ctypes.c_int64 * 2
+    status = csa.lib.csa_cache_insert(ctypes.byref(d), ctypes.c_void_p(k), two(*k_stride), ctypes.c_void_p(v),
+                                      two(*v_stride), None)
+    return status, csa.csa_last_error_string()
+
+
+K0, V0, FREE = 1 << 20, 1 << 30, 1 << 40  # addresses that nothing reads: each call is refused before
+
+
+def test_insert_refuses_rows_of_the_cache(csa):
+    """New rows out of the cache itself could be read after their slot was written."""
+    d = _cache(csa)
+    row = (256, 64)
+    slot0 = (8192, 2048)  # slot 0 of each unit, as a view
+    for k, ks, v, vs in [(K0, slot0, FREE, row), (FREE, row, V0, slot0), (V0, slot0, FREE, row),
+                         (K0 + 2 * 64 * 31, slot0, FREE, row), (K0, (0, 0), FREE, row),
+                         (K0 - 2, row, FREE, row)]:
+        status, why = _insert(csa, d, k, ks, v, vs)
+        assert status == INVALID and "overlap" in why, why
+    # beside the cache, and in the same buffer between its rows (a slot that is not the cache's)
+    between = _cache(csa, T=31, budget=31)
+    for dd, k, ks in [(d, K0 + 2 * 64 * 32 * 8, row), (d, K0 - 2 * 64 * 8, row), (between, K0 + 2 * 64 * 31, slot0)]:
+        status, why = _insert(csa, dd, k, ks, FREE, row)
+        assert "overlap" not in why, why  # (refused later on: no such memory)
+
+
+def test_cache_refuses_slots_that_overlap(csa):
+    for kw in (dict(k_stride=(64, 2048, 64)), dict(v_stride=(2048, 2048, 64)), dict(k_stride=(0, 2048, 64)),
+               dict(V=K0), dict(V=K0 + 2 * 64 * 32 * 4), dict(V=K0 + 126)):
+        d = _cache(csa, **kw)
+        status, why = _insert(csa, d, FREE, (256, 64), FREE, (256, 64))
+        assert status == INVALID and "overlap" in why, (kw, why)
+        src = csa.cache_source(S=0)
+        assert csa.lib.csa_cache_compress(ctypes.byref(d), ctypes.byref(src), None) == INVALID
+        assert "overlap" in csa.csa_last_error_string(), kw
+    # K and V in one buffer, a slot's key and value side by side
+    d = _cache(csa, V=K0 + 128, k_stride=(16384, 4096, 128), v_stride=(16384, 4096, 128))
+    assert "overlap" not in _insert(csa, d, FREE, (256, 64), FREE, (256, 64))[1]
