@@ -651,7 +651,8 @@ CSA_API csa_status csa_rotary_table(int rot, double theta, int scaling, double f
  * integers, so far positions keep their accuracy; sums are fp32.
  *   x, y [B, S, H, D] of `dtype` by strides in elements (batch, token, head;
  *   the last index dense).  y == x with equal strides turns in place; other
- *   overlaps are not allowed.  H2 = 0: no second tensor.  x and y need only
+ *   overlaps, of an output with an input, with the other output or among its
+ *   own rows, are refused.  H2 = 0: no second tensor.  x and y need only
  *   their element's alignment (CSA_ROTARY_INTERLEAVED: two elements').
  *   D even, D <= 512;  rot even, 2 <= rot <= D;  strides non-negative, and even for
  *   CSA_ROTARY_INTERLEAVED, y's not below D (distinct rows);  B * S * D <= 2^29;

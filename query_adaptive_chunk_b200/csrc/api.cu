@@ -1204,10 +1204,8 @@ csa_status rotary_tensor(const csa_rotary_desc* d, const void* x, void* y, int H
       CSA_SUPPORT(xs[i] % 2 == 0 && ys[i] % 2 == 0, nm + ": interleaved pairs need even strides");
   for (int i = 0; i < 3; ++i)
     CSA_REQUIRE(n[i] <= 1 || ys[i] >= d->D, nm + " output: rows overlap (a stride is below D)");
-  const bool same = x == y && xs[0] == ys[0] && xs[1] == ys[1] && xs[2] == ys[2];
   CSA_TRY(check_ptr(x, name, true, es));
   CSA_TRY(check_ptr(y, (nm + " output").c_str(), true, es));
-  CSA_REQUIRE(x != y || same, nm + ": in place needs equal strides");
   t->x = x;
   t->y = y;
   t->H = H;
@@ -1215,6 +1213,33 @@ csa_status rotary_tensor(const csa_rotary_desc* d, const void* x, void* y, int H
     t->xst[i] = xs[i];
     t->yst[i] = ys[i];
   }
+  return CSA_OK;
+}
+
+// No output row may share memory with another, nor with an input row, except
+// that a tensor may be turned in place.
+csa_status rotary_apart(const csa_rotary_desc* d) {
+  csa::Rows in[2], out[2];
+  int n = 0;
+  bool in_place[2];
+  auto take = [&](const void* x, const void* y, int H, const int64_t* xs, const int64_t* ys) {
+    if (H <= 0 || x == nullptr || y == nullptr) return;
+    for (int i = 0; i < 3; ++i)
+      if (xs[i] < 0 || ys[i] < 0) return;  // refused as strides
+    const int es = dtype_size(d->dtype);
+    in[n] = csa::Rows{x, 3, {d->B, d->S, H}, {xs[0], xs[1], xs[2]}, d->D, es};
+    out[n] = csa::Rows{y, 3, {d->B, d->S, H}, {ys[0], ys[1], ys[2]}, d->D, es};
+    in_place[n++] = x == y && xs[0] == ys[0] && xs[1] == ys[1] && xs[2] == ys[2];
+  };
+  take(d->x, d->y, d->H, d->x_stride, d->y_stride);
+  take(d->x2, d->y2, d->H2, d->x2_stride, d->y2_stride);
+  for (int i = 0; i < n; ++i) {
+    CSA_REQUIRE(!csa::rows_meet_themselves(out[i]), "output rows overlap");
+    for (int k = 0; k < n; ++k)
+      CSA_REQUIRE((i == k && in_place[i]) || !csa::rows_meet(out[i], in[k]),
+                  "an output overlaps an input that is not turned in place");
+  }
+  if (n == 2) CSA_REQUIRE(!csa::rows_meet(out[0], out[1]), "the outputs overlap");
   return CSA_OK;
 }
 
@@ -1377,6 +1402,7 @@ csa_status csa_rotary(const csa_rotary_desc* d, csa_stream stream) {
   CSA_SUPPORT(d->S <= (1ll << 30) && static_cast<int64_t>(d->B) * d->S <= (1ll << 29) / d->D,
               "B * S * D must be <= 2^29");
   CSA_SUPPORT(d->H <= 65535 && d->H2 <= 65535, "H and H2 must be <= 65535");
+  CSA_TRY(rotary_apart(d));
   csa::RotaryArgs a;
   if (d->H > 0) CSA_TRY(rotary_tensor(d, d->x, d->y, d->H, d->x_stride, d->y_stride, "x", &a.t[0]));
   if (d->H2 > 0)

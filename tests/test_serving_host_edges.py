@@ -77,3 +77,33 @@ def test_cache_refuses_slots_that_overlap(csa):
     # K and V in one buffer, a slot's key and value side by side
     d = _cache(csa, V=K0 + 128, k_stride=(16384, 4096, 128), v_stride=(16384, 4096, 128))
     assert "overlap" not in _insert(csa, d, FREE, (256, 64), FREE, (256, 64))[1]
+
+
+def _rotary(csa, **kw):
+    d = dict(B=2, S=5, H=4, H2=2, D=64, rot=32, dtype=1, amplitude=1.0, x=K0, y=V0, x2=FREE, y2=FREE + (1 << 20))
+    d.update({f"{t}_stride": (5 * 256, 256, 64) for t in ("x", "y")})
+    d.update({f"{t}_stride": (5 * 128, 128, 64) for t in ("x2", "y2")})
+    d.update(kw)
+    status = csa.lib.csa_rotary(ctypes.byref(csa.rotary_desc(**d)), None)
+    return status, csa.csa_last_error_string()
+
+
+def test_rotary_refuses_outputs_over_other_rows(csa):
+    """A thread's row could be written before another thread reads it."""
+    head = 2 * 64
+    packed = dict(x=K0, x2=K0 + 4 * head, x_stride=(5 * 512, 512, 64), x2_stride=(5 * 512, 512, 64))
+    for kw in (dict(y=K0 + head),                                   # a head further on in its own input
+               dict(y=K0 + 2), dict(y=K0 - 2),
+               dict(y=K0, y_stride=(5 * 256, 256 // 4, 5 * 64)),    # in place in another order
+               dict(x2=V0), dict(y2=K0), dict(y2=V0),               # over the other tensor
+               dict(packed, y=K0 + 4 * head, y_stride=(5 * 512, 512, 64)),
+               dict(y_stride=(64, 64, 64)), dict(y2_stride=(128, 128, 64)),  # rows of one output
+               dict(x2=K0, x2_stride=(5 * 256, 256, 64), y=K0)):    # turned in place and read besides
+        status, why = _rotary(csa, **kw)
+        assert status == INVALID and "overlap" in why, (kw, why)
+    own = dict(packed, y=K0, y2=K0 + 4 * head, y_stride=(5 * 512, 512, 64), y2_stride=(5 * 512, 512, 64))
+    for kw in ({}, own, dict(packed, y=K0, y_stride=(5 * 512, 512, 64)), dict(x_stride=(0, 256, 64)),
+               dict(x2=K0), dict(packed, y=K0 + 6 * head, x_stride=(5 * 1024, 1024, 64), x2_stride=(5 * 1024, 1024, 64),
+                                 y_stride=(5 * 1024, 1024, 64))):
+        status, why = _rotary(csa, **kw)
+        assert "overlap" not in why, (kw, why)  # (refused later on: no such memory)
