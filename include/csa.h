@@ -743,7 +743,8 @@ CSA_API csa_status csa_cache_insert(const csa_cache_desc* c, const void* k,
  *   src K, V by strides (sequence, head, row); weights [B, Hkv, S] fp32;
  *   positions NULL (the row number) or [B, Hkv, S] int32; src_next_pos NULL
  *   (n) or [B], required with positions.  n_sink + n_local <= budget.
- *   Source and cache (len among them) must not overlap.  S < 2^31 - 65536; c->counters is
+ *   Source and cache must share no row and no other entry (refused), except that
+ *   src_next_pos, or without it src_len, may be c->next_pos.  S < 2^31 - 65536; c->counters is
  *   not used. */
 typedef struct csa_cache_source {
   const void* K;

@@ -1464,16 +1464,29 @@ csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* s
   CSA_SUPPORT(s->S < 2147483648LL - 65536, "S must be < 2^31 - 65536");
   CSA_REQUIRE(s->positions == nullptr || s->next_pos != nullptr,
               "source positions need the source's next_pos");
-  if (s->len != nullptr) {
-    Extent x, y;
-    x.lo = reinterpret_cast<uintptr_t>(s->len);
-    x.hi = x.lo + static_cast<uintptr_t>(c->B) * 4;
-    y.lo = reinterpret_cast<uintptr_t>(c->len);
-    y.hi = y.lo + static_cast<uintptr_t>(c->B) * 4;
-    CSA_REQUIRE(!x.overlaps(y), "the source's len must not be the cache's");
-  }
+  // [B] arrays: none that is read may share memory with one that is written, but
+  // a next_pos or len may be the cache's next_pos where it is written back unchanged
+  auto meet = [&](const int32_t* x, const int32_t* y) {
+    return x && y && x < y + c->B && y < x + c->B;
+  };
+  CSA_REQUIRE(!meet(s->len, c->len), "the source's len must not be the cache's");
+  CSA_REQUIRE(!meet(s->next_pos, c->len), "the source's next_pos must not be the cache's len");
+  CSA_REQUIRE(!meet(s->next_pos, c->next_pos) || s->next_pos == c->next_pos,
+              "the source's next_pos overlaps the cache's");
+  CSA_REQUIRE(!meet(s->len, c->next_pos) || (s->len == c->next_pos && s->next_pos == nullptr),
+              "the source's len overlaps the cache's next_pos");
   if (c->B == 0) return CSA_OK;
   CSA_TRY(cache_slots_apart(c));
+  for (int i = 0; i < 2; ++i)
+    for (int is_v = 0; is_v < 2; ++is_v) {
+      const void* p = i ? s->V : s->K;
+      const int64_t* st = i ? s->v_stride : s->k_stride;
+      if (s->S == 0 || p == nullptr || st[0] < 0 || st[1] < 0 || st[2] < 0) continue;  // (refused below)
+      CSA_REQUIRE(!csa::rows_meet(csa::Rows{p, 3, {c->B, c->Hkv, s->S}, {st[0], st[1], st[2]}, c->D,
+                                            dtype_size(c->dtype)},
+                                  cache_rows(c, is_v)),
+                  "source and cache overlap");
+    }
   Extent ek, ev, sk, sv;
   CSA_TRY(cache_ptrs(c, false, &ek, &ev));
   if (s->S > 0) {
@@ -1494,9 +1507,7 @@ csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* s
     };
     const Extent dw = dense(c->weights, c->T), dp = dense(c->positions, c->T);
     const Extent sw = dense(s->weights, s->S);
-    CSA_REQUIRE(!sk.overlaps(ek) && !sk.overlaps(ev) && !sv.overlaps(ek) && !sv.overlaps(ev) &&
-                    !sw.overlaps(dw) && !sw.overlaps(dp),
-                "source and cache overlap");
+    CSA_REQUIRE(!sw.overlaps(dw) && !sw.overlaps(dp), "source and cache overlap");
     if (s->positions) {
       const Extent sp = dense(s->positions, s->S);
       CSA_REQUIRE(!sp.overlaps(dp) && !sp.overlaps(dw), "source and cache overlap");

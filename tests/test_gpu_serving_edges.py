@@ -144,3 +144,24 @@ def test_compress_of_paused_sequences(steps, csa, B, Hkv, Sn, T, n_sink, n_local
                 want = pos[b, h, rows] if given else rows
                 assert cache.positions[b, h, :len(rows)].tolist() == list(want)
                 assert torch.equal(cache.K[b, h, :len(rows)], K[b, h, rows])
+
+
+def test_compress_within_one_buffer(steps, csa):
+    """The cache is the first slots of each unit's storage, the source the others."""
+    B, Hkv, T, Sn, D = 3, 2, 20, 90, 64
+    K, V = _randn((B, Hkv, T + Sn, D), 1, torch.bfloat16), _randn((B, Hkv, T + Sn, D), 2, torch.bfloat16)
+    w = torch.rand(B, Hkv, Sn, device="cuda")
+    Ks, Vs = K[:, :, T:], V[:, :, T:]
+    source = Ks.clone(), Vs.clone()
+    cache = steps.TokenCache(K[:, :, :T], V[:, :, :T], n_sink=2, n_local=5, next_pos=_i32([Sn, 40, 3]))
+    cache.compress(Ks, Vs, w, lengths=cache.next_pos)
+    csa.csa_check_device_status()
+    assert cache.next_pos.tolist() == [Sn, 40, 3] and cache.lengths.tolist() == [T, T, 3]
+    kept = S.cache_compress(to_np(w), [Sn, 40, 3], T, 2, 5)
+    for b in range(B):
+        for h in range(Hkv):
+            rows = kept[b][h]
+            assert cache.positions[b, h, :len(rows)].tolist() == rows
+            for x, s in ((K, source[0]), (V, source[1])):
+                assert torch.equal(x[b, h, :len(rows)], s[b, h, rows])
+    assert torch.equal(K[:, :, T:], source[0]) and torch.equal(V[:, :, T:], source[1])

@@ -107,3 +107,37 @@ def test_rotary_refuses_outputs_over_other_rows(csa):
                                  y_stride=(5 * 1024, 1024, 64))):
         status, why = _rotary(csa, **kw)
         assert "overlap" not in why, (kw, why)  # (refused later on: no such memory)
+
+
+def _compress(csa, d, **kw):
+    src = dict(S=40, K=FREE, V=FREE + (1 << 24), k_stride=(4 * 40 * 64, 40 * 64, 64), v_stride=(4 * 40 * 64, 40 * 64, 64),
+               weights=FREE + (1 << 25))
+    src.update(kw)
+    s = csa.cache_source(**src)
+    status = csa.lib.csa_cache_compress(ctypes.byref(d), ctypes.byref(s), None)
+    return status, csa.csa_last_error_string()
+
+
+def test_compress_takes_rows_beside_the_cache(csa):
+    """One buffer of 72 slots a unit: the first 32 are the cache, the rest the source."""
+    unit = 72 * 64
+    st = (4 * unit, unit, 64)
+    d = _cache(csa, k_stride=st, v_stride=st)
+    beside = dict(K=K0 + 32 * 128, V=V0 + 32 * 128, k_stride=st, v_stride=st)
+    assert "overlap" not in _compress(csa, d, **beside)[1]
+    for kw in (dict(beside, K=K0 + 31 * 128), dict(beside, V=V0 + 32 * 128 - 2), dict(beside, V=K0), dict(beside, S=41)):
+        status, why = _compress(csa, d, **kw)
+        assert status == INVALID and "overlap" in why, kw
+
+
+def test_compress_refuses_lengths_that_it_writes(csa):
+    """Every head reads the source's length and one of them writes the cache's state."""
+    L, P = 1 << 41, 1 << 42
+    d = _cache(csa, B=8, Hkv=1, len=L, next_pos=P, k_stride=(2048, 2048, 64), v_stride=(2048, 2048, 64))
+    free = 1 << 43
+    for kw, word in [(dict(len=L), "len"), (dict(len=L + 16), "len"), (dict(next_pos=L), "next_pos"), (dict(next_pos=P - 16), "next_pos"),
+                     (dict(len=P, next_pos=free), "next_pos"), (dict(len=P + 16), "next_pos")]:
+        status, why = _compress(csa, d, **kw)
+        assert status == INVALID and word in why and "CUDA" not in why, (kw, why)
+    for kw in (dict(len=P), dict(next_pos=P), dict(len=free, next_pos=P), dict(len=L + 32, next_pos=P + 32)):
+        assert "CUDA" in _compress(csa, d, **kw)[1], kw  # goes on to the pointers
