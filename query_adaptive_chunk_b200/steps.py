@@ -342,6 +342,34 @@ def _dense(name, t, dtype, shape):
     return t
 
 
+class _Turn(torch.autograd.Function):
+    """Rotary.rotate for autograd: linear, so the gradient is the transposed
+    rotation of the outputs' (and in its turn differentiable)."""
+
+    @staticmethod
+    def forward(ctx, rotary, transpose, pos0, positions, q, k):
+        ctx.set_materialize_grads(False)
+        # the positions of the forward pass, whatever becomes of the caller's (a
+        # cache's next_pos advances in place)
+        ctx.rotary, ctx.transpose, ctx.pos0 = rotary, transpose, pos0
+        ctx.positions = None if positions is None else positions.clone()
+        return rotary.rotate(q, k, positions=positions, pos0=pos0, transpose=transpose)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        out = [None, None]
+        need = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[4 + i]]
+        if need:
+            # any strides and offset may come back (of an expanded sum: all zero)
+            gs = [grads[i] if grads[i].stride(-1) == 1
+                  and all(s % 2 == 0 for s in (*grads[i].stride()[:-1], grads[i].storage_offset()))
+                  else grads[i].clone(memory_format=torch.contiguous_format) for i in need]
+            y = ctx.rotary.rotate(*gs, positions=ctx.positions, pos0=ctx.pos0, transpose=not ctx.transpose)
+            for i, g in zip(need, y if len(need) == 2 else (y,)):
+                out[i] = g
+        return None, None, None, None, *out
+
+
 class Rotary:
     """Rotary positions (csa_rotary) with one frequency table.
 
@@ -371,8 +399,14 @@ class Rotary:
         [B, S] (rows may repeat: expand a [1, S]), else pos0 + s.  Results go to
         q_out / k_out (q_out=q: in place), by default new tensors of `stream`
         (then a torch stream).
-        transpose=True gives the gradient of the input from that of the output.
+        transpose=True gives the gradient of the input from that of the output; autograd
+        finds it by itself through q and k that require gradients, on the current
+        stream and with new outputs (anything else is refused then).
         Returns (q_out, k_out), or q_out alone without k."""
+        if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+            if q_out is not None or k_out is not None or stream is not None:
+                _bad("q or k requires a gradient: no q_out, k_out or stream (detach them, or use torch.no_grad)")
+            return _Turn.apply(self, transpose, pos0, positions, q, k)
         B, S, Hq, D = q.shape
         dt, dev = q.dtype, self.table.device
         if dt not in _TYPES:
@@ -527,10 +561,11 @@ class SharedPrefixDecoder:
 
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None):
         """One decode step: q [B, Hq, D] and k [B, Hkv, D] are turned to the next
-        position (when there is a rotary), k and v enter the cache, and q attends."""
+        position (when there is a rotary), k and v enter the cache, and q attends.
+        For serving: no gradient is kept."""
         c = self.cache
         if self.rotary is not None:
-            self.rotary.rotate(q[:, None], k[:, None], positions=c.next_pos[:, None],
+            self.rotary.rotate(q.detach()[:, None], k.detach()[:, None], positions=c.next_pos[:, None],
                                q_out=self.q[:, None], k_out=self.k[:, None], stream=stream)
             q, k = self.q, self.k
         c.insert(k, v, stream=stream)

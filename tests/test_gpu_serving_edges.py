@@ -165,3 +165,137 @@ def test_compress_within_one_buffer(steps, csa):
             for x, s in ((K, source[0]), (V, source[1])):
                 assert torch.equal(x[b, h, :len(rows)], s[b, h, rows])
     assert torch.equal(K[:, :, T:], source[0]) and torch.equal(V[:, :, T:], source[1])
+
+
+# ---------------------------------------------------------------- gradients of the rotation
+
+def _tol(x, amp):
+    """Of a turned tensor: 6e-7 A (|x_a| + |x_b|) and the result's rounding (the bound of the
+    forward tests), over all its values."""
+    u = U16 if x.dtype == torch.bfloat16 else U32
+    return float((2 * 6e-7 + u * math.sqrt(2)) * amp * x.abs().max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("what", ["both", "q", "k", "no k", "unused k", "expanded"])
+def test_rotary_autograd(steps, dtype, layout, what):
+    """Gradients flow through rotate() as the formula says, from packed projections, for
+    positions that change after the forward pass."""
+    B, Sq, Hq, Hkv, D, rot, amp = 2, 33, 6, 2, 64, 48, 1.25
+    packed = _randn((B, Sq, (Hq + 2 * Hkv) * D), 7, DT[dtype])
+    need = {"q": (True, False), "k": (False, True)}.get(what, (True, True))
+    q0 = packed[..., :Hq * D].view(B, Sq, Hq, D).clone().requires_grad_(need[0])
+    k0 = packed[..., Hq * D:(Hq + Hkv) * D].view(B, Sq, Hkv, D).clone().requires_grad_(need[1])
+    q, k = q0.transpose(1, 2).contiguous().transpose(1, 2), k0 * 1  # head-major, and a plain copy
+    pos = np.random.default_rng(3).integers(0, 1 << 20, (B, Sq))
+    p = _i32(pos.tolist())
+    r = steps.Rotary(rot, layout=layout, amplitude=amp)
+    w = S.rotary_freqs(rot, 10000.0)
+    with torch.no_grad():
+        plain = r.rotate(q, positions=p) if what == "no k" else r.rotate(q, k, positions=p)
+    y = r.rotate(q, None if what == "no k" else k, positions=p)
+    yq, yk = (y, None) if what == "no k" else y
+    assert torch.equal(yq, plain if what == "no k" else plain[0])
+    assert yq.requires_grad and (yk is None or yk.requires_grad)
+    p.zero_()  # the gradient is that of the positions that were turned by
+    gq, gk = _randn((B, Sq, Hq, D), 8, DT[dtype]), _randn((B, Sq, Hkv, D), 9, DT[dtype])
+    if what == "expanded":
+        gq, gk = torch.ones_like(gq), torch.ones_like(gk)
+        loss = yq.sum() + yk.sum()
+    else:
+        loss = (yq * gq).sum() + (0 if yk is None or what == "unused k" else (yk * gk).sum())
+    loss.backward()
+    for x, g, used in ((q0, gq, need[0]), (k0, gk, need[1] and what not in ("no k", "unused k"))):
+        if not used:
+            assert x.grad is None or not x.grad.any()
+            continue
+        want = S.rotary(to_np(g), pos, w, layout, amp, transpose=True)
+        want[..., rot:] = to_np(g)[..., rot:]
+        assert np.abs(to_np(x.grad) - want).max() <= _tol(g, amp)
+
+
+def test_rotary_autograd_against_differences(steps):
+    """Central differences of a linear map are exact up to rounding, and the gradient is
+    itself differentiable."""
+    B, Sq, H, D, amp = 1, 3, 2, 8, 0.75
+    r = steps.Rotary(6, theta=100.0, layout="interleaved", amplitude=amp)
+    x, c = _randn((B, Sq, H, D), 1).requires_grad_(), _randn((B, Sq, H, D), 2).requires_grad_()
+    f = lambda x, c: (r.rotate(x, pos0=11) * c).sum()
+    g, = torch.autograd.grad(f(x, c), x, create_graph=True)
+    num = torch.zeros_like(x)
+    with torch.no_grad():
+        for i in np.ndindex(*x.shape):
+            e = torch.zeros_like(x)
+            e[i] = 1.0
+            num[i] = ((r.rotate(x + e, pos0=11) - r.rotate(x - e, pos0=11)).double() * c.double()).sum() / 2
+    # each difference: two roundings of values below 8 and the rotation's 6e-7 of |x| sums, times c
+    assert float((g.detach() - num).abs().max()) <= 8 * (U32 + 2 * 6e-7) * float(c.detach().abs().max()) * 2
+    v = _randn(x.shape, 3)
+    h, = torch.autograd.grad((g * v).sum(), c)  # d/dc of c . rotate(v)
+    with torch.no_grad():
+        assert torch.equal(h, r.rotate(v, pos0=11))
+
+
+@pytest.mark.parametrize("pad", [(1, 1), (1, 2), (2, 2), (0, 3)])
+def test_rotary_autograd_of_a_narrow_gradient(steps, pad):
+    """The gradient comes back as a view of a wider one, off the pairs' alignment."""
+    x = _randn((2, 5, 3, 64), 1, torch.bfloat16).requires_grad_()
+    c = _randn((2, 5, 3, 64 + sum(pad)), 2, torch.bfloat16)
+    r = steps.Rotary(64, layout="interleaved")
+    parts = [torch.zeros(2, 5, 3, n, dtype=x.dtype, device="cuda") for n in pad]
+    (torch.cat([parts[0], r.rotate(x, pos0=3), parts[1]], -1) * c).sum().backward()
+    with torch.no_grad():
+        want = r.rotate(c[..., pad[0]:pad[0] + 64].contiguous(), pos0=3, transpose=True)
+    assert torch.equal(x.grad, want)
+
+
+def test_rotary_autograd_in_a_graph(steps):
+    """A captured training step gives the eager one's gradients on new inputs."""
+    r = steps.Rotary(64, theta=10000.0)
+    x, g = _randn((2, 17, 4, 64), 1), _randn((2, 17, 4, 64), 2)
+    k, gk = _randn((2, 17, 1, 64), 3), _randn((2, 17, 1, 64), 4)
+    p = torch.arange(17, dtype=torch.int32, device="cuda").expand(2, 17)
+
+    def step():
+        xi, ki = x.detach().requires_grad_(), k.detach().requires_grad_()
+        y, z = r.rotate(xi, ki, positions=p)
+        return torch.autograd.grad([y, z], [xi, ki], [g, gk])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="relaxed"):
+        out = step()
+    g.copy_(_randn(g.shape, 5))
+    graph.replay()
+    want = step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_rotary_refuses_what_autograd_cannot_see(steps, csa):
+    r = steps.Rotary(64)
+    x = _randn((1, 4, 2, 64), 1).requires_grad_()
+    for kw in (dict(q_out=torch.empty_like(x)), dict(stream=torch.cuda.Stream())):
+        with pytest.raises(csa.CsaError):
+            r.rotate(x, **kw)
+    with pytest.raises(csa.CsaError):
+        r.rotate(x.detach(), x, k_out=torch.empty_like(x))
+    with torch.no_grad():
+        y = torch.empty_like(x)
+        assert r.rotate(x, q_out=y) is y and not y.requires_grad
+
+
+def test_step_takes_outputs_of_a_model_in_training_mode(steps, csa):
+    K = _randn((2, 2, 16, 64), 1)
+    cache = steps.TokenCache(K, K.clone())
+    dec = steps.SharedPrefixDecoder(cache, Hq=4, rotary=steps.Rotary(64))
+    q, k, v = (_randn((2, n, 64), n).requires_grad_() for n in (4, 2, 2))
+    out, _ = dec.step(q, k, v)
+    csa.csa_check_device_status()
+    assert not out.requires_grad and torch.equal(out.view(2, 2, 2, 64), v.detach()[:, :, None].expand(2, 2, 2, 64))
