@@ -606,6 +606,9 @@ CSA_API csa_status csa_block_sparse_prefill(const void* Q, const void* K, const 
                                     int S, int Hq, int Hkv, int D, int tile_m, int L,
                                     float scale, void* O, csa_stream stream);
 
+/* In the calls from here on, the stride of an index that has one entry only is not
+ * used and may be anything. */
+
 /* ---------------------------------------------------------------- rotary positions
  * The full form of csa_rope for a serving or training loop (no counterpart in
  * the pages beyond RoPE itself): both pair layouts, part of the head, scaled

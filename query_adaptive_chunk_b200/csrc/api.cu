@@ -1175,13 +1175,16 @@ struct Extent {
   uintptr_t lo = 0, hi = 0;
   bool overlaps(const Extent& o) const { return lo < o.hi && o.lo < hi; }
 };
+// The stride of an index of n entries: that of a single one is never used, and
+// views leave it at any value.
+int64_t used(int64_t n, int64_t stride) { return n > 1 ? stride : 0; }
 // Strides must be non-negative and the whole extent below 2^62 bytes.
 bool extent_of(const void* p, const int64_t* n, const int64_t* st, int dims, int64_t last, int es,
                Extent* x) {
   __int128 most = last - 1;
   for (int i = 0; i < dims; ++i) {
-    if (st[i] < 0) return false;
-    if (n[i] > 0) most += static_cast<__int128>(n[i] - 1) * st[i];
+    if (used(n[i], st[i]) < 0) return false;
+    if (n[i] > 0) most += static_cast<__int128>(n[i] - 1) * used(n[i], st[i]);
   }
   if (most >= (static_cast<__int128>(1) << 60)) return false;
   x->lo = reinterpret_cast<uintptr_t>(p);
@@ -1201,7 +1204,8 @@ csa_status rotary_tensor(const csa_rotary_desc* d, const void* x, void* y, int H
               nm + ": strides must be non-negative");
   if (d->layout == CSA_ROTARY_INTERLEAVED)
     for (int i = 0; i < 3; ++i)
-      CSA_SUPPORT(xs[i] % 2 == 0 && ys[i] % 2 == 0, nm + ": interleaved pairs need even strides");
+      CSA_SUPPORT(used(n[i], xs[i]) % 2 == 0 && used(n[i], ys[i]) % 2 == 0,
+                  nm + ": interleaved pairs need even strides");
   for (int i = 0; i < 3; ++i)
     CSA_REQUIRE(n[i] <= 1 || ys[i] >= d->D, nm + " output: rows overlap (a stride is below D)");
   CSA_TRY(check_ptr(x, name, true, es));
@@ -1210,8 +1214,8 @@ csa_status rotary_tensor(const csa_rotary_desc* d, const void* x, void* y, int H
   t->y = y;
   t->H = H;
   for (int i = 0; i < 3; ++i) {
-    t->xst[i] = xs[i];
-    t->yst[i] = ys[i];
+    t->xst[i] = used(n[i], xs[i]);
+    t->yst[i] = used(n[i], ys[i]);
   }
   return CSA_OK;
 }
@@ -1224,12 +1228,18 @@ csa_status rotary_apart(const csa_rotary_desc* d) {
   bool in_place[2];
   auto take = [&](const void* x, const void* y, int H, const int64_t* xs, const int64_t* ys) {
     if (H <= 0 || x == nullptr || y == nullptr) return;
-    for (int i = 0; i < 3; ++i)
-      if (xs[i] < 0 || ys[i] < 0) return;  // refused as strides
-    const int es = dtype_size(d->dtype);
-    in[n] = csa::Rows{x, 3, {d->B, d->S, H}, {xs[0], xs[1], xs[2]}, d->D, es};
-    out[n] = csa::Rows{y, 3, {d->B, d->S, H}, {ys[0], ys[1], ys[2]}, d->D, es};
-    in_place[n++] = x == y && xs[0] == ys[0] && xs[1] == ys[1] && xs[2] == ys[2];
+    const int64_t count[3] = {d->B, d->S, H};
+    in[n] = csa::Rows{x, 3, {d->B, d->S, H}, {}, d->D, dtype_size(d->dtype)};
+    out[n] = in[n];
+    out[n].p = y;
+    in_place[n] = x == y;
+    for (int i = 0; i < 3; ++i) {
+      in[n].st[i] = used(count[i], xs[i]);
+      out[n].st[i] = used(count[i], ys[i]);
+      if (in[n].st[i] < 0 || out[n].st[i] < 0) return;  // refused as strides
+      in_place[n] = in_place[n] && in[n].st[i] == out[n].st[i];
+    }
+    ++n;
   };
   take(d->x, d->y, d->H, d->x_stride, d->y_stride);
   take(d->x2, d->y2, d->H2, d->x2_stride, d->y2_stride);
@@ -1288,7 +1298,11 @@ csa_status cache_ptrs(const csa_cache_desc* c, bool insert, Extent* ek, Extent* 
 // The slots of the cache's K (is_v = false) or V.
 csa::Rows cache_rows(const csa_cache_desc* c, bool is_v) {
   const int64_t* st = is_v ? c->v_stride : c->k_stride;
-  return csa::Rows{is_v ? c->V : c->K, 3, {c->B, c->Hkv, c->T}, {st[0], st[1], st[2]}, c->D,
+  return csa::Rows{is_v ? c->V : c->K,
+                   3,
+                   {c->B, c->Hkv, c->T},
+                   {used(c->B, st[0]), used(c->Hkv, st[1]), used(c->T, st[2])},
+                   c->D,
                    dtype_size(c->dtype)};
 }
 
@@ -1307,9 +1321,10 @@ csa::CacheArgs cache_args(const csa_cache_desc* c) {
   csa::CacheArgs a{};
   a.K = c->K;
   a.V = c->V;
+  const int64_t n[3] = {c->B, c->Hkv, c->T};
   for (int i = 0; i < 3; ++i) {
-    a.kst[i] = c->k_stride[i];
-    a.vst[i] = c->v_stride[i];
+    a.kst[i] = used(n[i], c->k_stride[i]);
+    a.vst[i] = used(n[i], c->v_stride[i]);
   }
   a.weights = c->weights;
   a.positions = c->positions;
@@ -1348,12 +1363,16 @@ csa_status prefix_sizes(csa_dtype dtype, int B, int Hq, int Hkv, int D, int N, i
   return CSA_OK;
 }
 
-csa_status strides16(const int64_t* st, int es, int64_t rows, int D, const char* name) {
+// Strides `st` of a [n0, n1, rows] of rows, as used, into `to`.
+csa_status strides16(const int64_t* st, int es, int64_t n0, int64_t n1, int64_t rows, int D,
+                     const char* name, int64_t* to) {
   CSA_SUPPORT(rows <= 1 || st[2] < 0 || st[2] >= D,
               std::string(name) + ": strides of the tokens must be at least D");
+  const int64_t n[3] = {n0, n1, rows};
   for (int i = 0; i < 3; ++i) {
-    CSA_REQUIRE(st[i] >= 0, std::string(name) + ": strides must be non-negative");
-    CSA_SUPPORT(st[i] * es % 16 == 0, std::string(name) + ": strides must be multiples of 16 bytes");
+    to[i] = used(n[i], st[i]);
+    CSA_REQUIRE(to[i] >= 0, std::string(name) + ": strides must be non-negative");
+    CSA_SUPPORT(to[i] * es % 16 == 0, std::string(name) + ": strides must be multiples of 16 bytes");
   }
   return CSA_OK;
 }
@@ -1435,10 +1454,12 @@ csa_status csa_cache_insert(const csa_cache_desc* c, const void* k, const int64_
   CSA_TRY(cache_slots_apart(c));
   const int es = dtype_size(c->dtype);
   const int64_t n[2] = {c->B, c->Hkv};
+  const int64_t kst[2] = {used(n[0], k_stride[0]), used(n[1], k_stride[1])};
+  const int64_t vst[2] = {used(n[0], v_stride[0]), used(n[1], v_stride[1])};
   for (int i = 0; i < 2; ++i)  // (units run side by side: one may write what another has yet to read)
     for (int is_v = 0; is_v < 2; ++is_v) {
       const void* p = i ? v : k;
-      const int64_t* st = i ? v_stride : k_stride;
+      const int64_t* st = i ? vst : kst;
       if (p == nullptr || st[0] < 0 || st[1] < 0) continue;  // refused below
       CSA_REQUIRE(!csa::rows_meet(csa::Rows{p, 2, {n[0], n[1], 0}, {st[0], st[1], 0}, c->D, es},
                                   cache_rows(c, is_v)),
@@ -1452,7 +1473,7 @@ csa_status csa_cache_insert(const csa_cache_desc* c, const void* k, const int64_
               "k / v: strides must be non-negative");
   csa::Launch l;
   CSA_TRY(launch_ctx(stream, &l));
-  return finish(csa::launch_cache_insert(l, cache_args(c), k, k_stride, v, v_stride),
+  return finish(csa::launch_cache_insert(l, cache_args(c), k, kst, v, vst),
                 "cache insert launch");
 }
 
@@ -1477,10 +1498,16 @@ csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* s
               "the source's len overlaps the cache's next_pos");
   if (c->B == 0) return CSA_OK;
   CSA_TRY(cache_slots_apart(c));
+  const int64_t sn[3] = {c->B, c->Hkv, s->S};
+  csa::CacheSource a{};
+  for (int i = 0; i < 3; ++i) {
+    a.kst[i] = used(sn[i], s->k_stride[i]);
+    a.vst[i] = used(sn[i], s->v_stride[i]);
+  }
   for (int i = 0; i < 2; ++i)
     for (int is_v = 0; is_v < 2; ++is_v) {
       const void* p = i ? s->V : s->K;
-      const int64_t* st = i ? s->v_stride : s->k_stride;
+      const int64_t* st = i ? a.vst : a.kst;
       if (s->S == 0 || p == nullptr || st[0] < 0 || st[1] < 0 || st[2] < 0) continue;  // (refused below)
       CSA_REQUIRE(!csa::rows_meet(csa::Rows{p, 3, {c->B, c->Hkv, s->S}, {st[0], st[1], st[2]}, c->D,
                                             dtype_size(c->dtype)},
@@ -1494,9 +1521,8 @@ csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* s
     CSA_TRY(check_ptr(s->K, "source K", true, es));
     CSA_TRY(check_ptr(s->V, "source V", true, es));
     CSA_TRY(check_ptr(s->weights, "source weights"));
-    const int64_t n[3] = {c->B, c->Hkv, s->S};
-    CSA_REQUIRE(extent_of(s->K, n, s->k_stride, 3, c->D, es, &sk) &&
-                    extent_of(s->V, n, s->v_stride, 3, c->D, es, &sv),
+    CSA_REQUIRE(extent_of(s->K, sn, s->k_stride, 3, c->D, es, &sk) &&
+                    extent_of(s->V, sn, s->v_stride, 3, c->D, es, &sv),
                 "source: strides must be non-negative");
     const uintptr_t rows = static_cast<uintptr_t>(c->B) * c->Hkv;
     auto dense = [&](const void* p, int64_t len) {
@@ -1516,13 +1542,8 @@ csa_status csa_cache_compress(const csa_cache_desc* c, const csa_cache_source* s
   CSA_TRY(check_ptr(s->positions, "source positions", false));
   CSA_TRY(check_ptr(s->len, "source len", false));
   CSA_TRY(check_ptr(s->next_pos, "source next_pos", false));
-  csa::CacheSource a{};
   a.K = s->K;
   a.V = s->V;
-  for (int i = 0; i < 3; ++i) {
-    a.kst[i] = s->k_stride[i];
-    a.vst[i] = s->v_stride[i];
-  }
   a.weights = s->weights;
   a.positions = s->positions;
   a.len = s->len;
@@ -1551,15 +1572,16 @@ csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream)
   CSA_REQUIRE(d->N <= 1 || d->group_start != nullptr, "group_start is required for N > 1");
   if (d->B == 0) return CSA_OK;
   const int es = dtype_size(d->dtype);
+  csa::PrefixDecodeArgs a{};
   if (d->N > 0 && d->Tp > 0) {
-    CSA_TRY(strides16(d->kp_stride, es, d->Tp, d->D, "Kp"));
-    CSA_TRY(strides16(d->vp_stride, es, d->Tp, d->D, "Vp"));
+    CSA_TRY(strides16(d->kp_stride, es, d->N, d->Hkv, d->Tp, d->D, "Kp", a.kps));
+    CSA_TRY(strides16(d->vp_stride, es, d->N, d->Hkv, d->Tp, d->D, "Vp", a.vps));
     CSA_TRY(check_ptr(d->Kp, "Kp"));
     CSA_TRY(check_ptr(d->Vp, "Vp"));
   }
   if (d->T > 0) {
-    CSA_TRY(strides16(d->k_stride, es, d->T, d->D, "K"));
-    CSA_TRY(strides16(d->v_stride, es, d->T, d->D, "V"));
+    CSA_TRY(strides16(d->k_stride, es, d->B, d->Hkv, d->T, d->D, "K", a.ks));
+    CSA_TRY(strides16(d->v_stride, es, d->B, d->Hkv, d->T, d->D, "V", a.vs));
     CSA_TRY(check_ptr(d->K, "K"));
     CSA_TRY(check_ptr(d->V, "V"));
   }
@@ -1579,7 +1601,6 @@ csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream)
                                         d->dtype == CSA_BF16, d->B, d->Hkv, G, d->D, d->N, d->Tp, d->T,
                                         d->weights != nullptr && d->T > 0, l.num_sms),
               "workspace smaller than csa_prefix_decode_workspace_bytes()");
-  csa::PrefixDecodeArgs a{};
   a.bf16 = d->dtype == CSA_BF16;
   a.out_bf16 = d->out_dtype == CSA_BF16;
   a.B = d->B;
@@ -1593,12 +1614,6 @@ csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream)
   a.Vp = d->Vp;
   a.K = d->K;
   a.V = d->V;
-  for (int i = 0; i < 3; ++i) {
-    a.kps[i] = d->kp_stride[i];
-    a.vps[i] = d->vp_stride[i];
-    a.ks[i] = d->k_stride[i];
-    a.vs[i] = d->v_stride[i];
-  }
   a.Tp = d->Tp;
   a.T = d->T;
   a.prefix_len = d->prefix_len;

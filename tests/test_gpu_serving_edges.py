@@ -299,3 +299,43 @@ def test_step_takes_outputs_of_a_model_in_training_mode(steps, csa):
     out, _ = dec.step(q, k, v)
     csa.csa_check_device_status()
     assert not out.requires_grad and torch.equal(out.view(2, 2, 2, 64), v.detach()[:, :, None].expand(2, 2, 2, 64))
+
+
+# ---------------------------------------------------------------- strides that are not used
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_odd_strides_of_single_entries(steps, csa, dtype):
+    """One prefix, one sequence, one token or one head out of wider buffers: the same bits
+    as from dense ones."""
+    dt = DT[dtype]
+
+    def odd(shape, seed):
+        """A tensor whose one-entry indices have strides that no row could start on."""
+        dense = _randn(shape, seed, dt)
+        st = [s if n > 1 else 3 + 2 * i for i, (n, s) in enumerate(zip(shape, dense.stride()))]
+        return dense, dense.as_strided(shape, st)
+
+    B, Hkv, T, Tp, D = 1, 1, 50, 200, 128
+    for G in (4, 12):
+        pairs = [odd(s, i) for i, s in enumerate([(B, Hkv, T, D), (B, Hkv, T, D), (1, Hkv, Tp, D), (1, Hkv, Tp, D)])]
+        q = _randn((B, Hkv * G, D), 9, dt)
+        got = []
+        for way in (0, 1):
+            K, V, Kp, Vp = (p[way] for p in pairs)
+            cache = steps.TokenCache(K, V, lengths=_i32([T]))
+            out, lse = steps.SharedPrefixDecoder(cache, Hq=Hkv * G, Kp=Kp, Vp=Vp).attend(q)
+            csa.csa_check_device_status()
+            got.append((out.clone(), lse.clone(), cache.weights.clone()))
+        assert all(torch.equal(x, y) for x, y in zip(*got))
+    r = steps.Rotary(64, layout="interleaved")
+    for shape in ((1, 1, 3, 64), (1, 7, 1, 64), (2, 1, 1, 64), (1, 1, 1, 64)):
+        dense, view = odd(shape, 3)
+        want = r.rotate(dense, pos0=5, q_out=torch.empty_like(dense))
+        assert torch.equal(r.rotate(view, pos0=5, q_out=torch.empty_like(dense)), want)
+        assert torch.equal(r.rotate(view, pos0=5, q_out=view), want) and torch.equal(dense, want)
+    (K, Kv), (V, Vv) = odd((1, 1, 8, 6), 1), odd((1, 1, 8, 6), 2)
+    (k, kv), (v, vv) = odd((1, 1, 6), 3), odd((1, 1, 6), 4)
+    cache = steps.TokenCache(Kv, Vv)
+    cache.insert(kv, vv)
+    csa.csa_check_device_status()
+    assert torch.equal(K[0, 0, 0], k[0, 0]) and torch.equal(V[0, 0, 0], v[0, 0])

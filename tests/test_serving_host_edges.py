@@ -141,3 +141,26 @@ def test_compress_refuses_lengths_that_it_writes(csa):
         assert status == INVALID and word in why and "CUDA" not in why, (kw, why)
     for kw in (dict(len=P), dict(next_pos=P), dict(len=free, next_pos=P), dict(len=L + 32, next_pos=P + 32)):
         assert "CUDA" in _compress(csa, d, **kw)[1], kw  # goes on to the pointers
+
+
+def test_strides_of_single_entries_are_not_used(csa):
+    """Views leave odd or no strides where an index has one entry; each call goes on
+    to its pointers."""
+    status, why = _rotary(csa, B=1, S=1, H2=0, layout=1, x_stride=(7, 5, 64), y_stride=(3, 0, 64))
+    assert "CUDA" in why, why
+    status, why = _rotary(csa, B=1, S=5, H=1, H2=0, x_stride=(-1, 128, 9), y_stride=(1, 128, 77))
+    assert "CUDA" in why, why
+    status, why = _rotary(csa, B=1, S=5, H=1, H2=0, x_stride=(5, 128, 3), y_stride=(9, 128, 0), y=K0)  # in place
+    assert "CUDA" in why, why
+    d = _cache(csa, B=1, Hkv=1, k_stride=(1, 3, 64), v_stride=(0, -5, 64))
+    assert "CUDA" in _insert(csa, d, FREE, (-1, 3), FREE, (0, 1))[1]
+    assert "CUDA" in _compress(csa, d, k_stride=(-1, 3, 64), v_stride=(1, 0, 64))[1]
+    two = dict(k_stride=(31, 33, 128), v_stride=(-2, 1, 128), kp_stride=(5, 7, 128), vp_stride=(-1, 0, 128))
+    kw = dict(dtype=1, B=1, Hq=4, Hkv=1, D=128, scale=0.1, N=1, Tp=128, T=64, decay=1.0, K=K0, V=V0, Kp=FREE, Vp=FREE, **two)
+    for change, word in [({}, "CUDA"), (dict(Tp=1, T=1, k_stride=(1, 1, 1), kp_stride=(1, 1, 1)), "CUDA"),
+                         (dict(B=2, N=0), "V: strides"), (dict(Hkv=2), "Kp: strides")]:
+        d = csa.prefix_decode_desc(**{**kw, **change})
+        if "V" in word:
+            d.k_stride = (ctypes.c_int64 * 3)(64 * 128, 1, 128)
+        assert csa.lib.csa_prefix_decode(ctypes.byref(d), None) in (INVALID, UNSUPPORTED)
+        assert word in csa.csa_last_error_string(), change
