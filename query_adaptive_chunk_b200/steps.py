@@ -342,6 +342,15 @@ def _dense(name, t, dtype, shape):
     return t
 
 
+def _wide_rows(name, t):
+    """What the decode's 16-byte accesses need of a cache or prefix [n0, n1, rows, D]."""
+    es = t.element_size()
+    if t.data_ptr() % 16 or any(s * es % 16 for n, s in zip(t.shape[:3], t.stride()) if n > 1):
+        _bad(f"{name}: rows must start on 16 bytes")
+    if t.shape[2] > 1 and t.stride(2) < t.shape[3]:
+        _bad(f"{name}: strides of the tokens must be at least D")
+
+
 class _Turn(torch.autograd.Function):
     """Rotary.rotate for autograd: linear, so the gradient is the transposed
     rotation of the outputs' (and in its turn differentiable)."""
@@ -523,10 +532,18 @@ class SharedPrefixDecoder:
         B, Hkv, T, D, dt, dev = cache.B, cache.Hkv, cache.T, cache.D, cache.K.dtype, cache.K.device
         self.cache, self.Hq, self.rotary = cache, Hq, rotary
         _typed("out_dtype", out_dtype)
+        scale = 1.0 / math.sqrt(D) if scale is None else scale
+        # what attend() would refuse on every call is refused here, before a step's insert
+        if not (math.isfinite(scale) and scale > 0):
+            _bad("scale must be finite and positive")
+        if not (math.isfinite(decay) and decay >= 0):
+            _bad("decay must be finite and non-negative")
         N = Tp = 0
         kw = {}
         if Kp is not None:
             N, _, Tp, _ = Kp.shape
+            if N > 1 and group_start is None:
+                _bad("group_start is required for more than one prefix")
             if Vp is None:
                 _bad("Kp without Vp")
             kw = dict(Kp=Kp, Vp=Vp, kp_stride=_rows("Kp", Kp, dt, (N, Hkv, Tp, D)),
@@ -535,6 +552,9 @@ class SharedPrefixDecoder:
                 kw["prefix_len"] = _dense("prefix_len", prefix_len, torch.int32, (N,))
             if group_start is not None:
                 kw["group_start"] = _dense("group_start", group_start, torch.int32, (N + 1,))
+        for name, t in (("K", cache.K), ("V", cache.V), ("Kp", Kp), ("Vp", Vp)):
+            if t is not None and t.numel() > 0:
+                _wide_rows(name, t)
         self.prefix = (Kp, Vp, prefix_len, group_start)  # kept alive with the descriptor
         _same_device(dev, Kp=Kp, Vp=Vp, prefix_len=prefix_len, group_start=group_start)
         self.out = torch.empty(B, Hq, D, dtype=out_dtype, device=dev)
@@ -545,16 +565,21 @@ class SharedPrefixDecoder:
             nbytes = csa.csa_prefix_decode_workspace_bytes(dt, B, Hq, Hkv, D, N, Tp, T, accumulate)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         self.desc = csa.prefix_decode_desc(
-            dtype=dt, B=B, Hq=Hq, Hkv=Hkv, D=D, scale=1.0 / math.sqrt(D) if scale is None else scale,
+            dtype=dt, B=B, Hq=Hq, Hkv=Hkv, D=D, scale=scale,
             N=N, Tp=Tp, T=T, K=cache.K, V=cache.V, k_stride=cache.k_stride, v_stride=cache.v_stride,
             len=cache.lengths, out=self.out, out_dtype=out_dtype, lse_out=self.lse,
             weights=cache.weights if accumulate else None, decay=decay, workspace=self.workspace,
             workspace_bytes=nbytes, next_pos=cache.next_pos, **kw)
 
+    def _check_q(self, q):
+        _dense("q", q, self.cache.K.dtype, self.out.shape)
+        if q.device != self.out.device or q.data_ptr() % 16:
+            _bad(f"q must be on {self.out.device} and start on 16 bytes")
+
     def attend(self, q: torch.Tensor, stream=None):
         """Attention of q [B, Hq, D] over the prefixes and the cache as they
         are; returns (out, lse), this decoder's buffers."""
-        _dense("q", q, self.cache.K.dtype, self.out.shape)
+        self._check_q(q)
         self.desc.q = q.data_ptr()
         csa.csa_prefix_decode(self.desc, stream=stream)
         return self.out, self.lse
@@ -568,5 +593,6 @@ class SharedPrefixDecoder:
             self.rotary.rotate(q.detach()[:, None], k.detach()[:, None], positions=c.next_pos[:, None],
                                q_out=self.q[:, None], k_out=self.k[:, None], stream=stream)
             q, k = self.q, self.k
+        self._check_q(q)  # before the cache changes
         c.insert(k, v, stream=stream)
         return self.attend(q, stream=stream)

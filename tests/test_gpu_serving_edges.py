@@ -339,3 +339,39 @@ def test_odd_strides_of_single_entries(steps, csa, dtype):
     cache.insert(kv, vv)
     csa.csa_check_device_status()
     assert torch.equal(K[0, 0, 0], k[0, 0]) and torch.equal(V[0, 0, 0], v[0, 0])
+
+
+# ---------------------------------------------------------------- refused steps
+
+@pytest.mark.parametrize("turned", [False, True])
+def test_a_refused_step_leaves_the_cache_as_it_was(steps, csa, turned):
+    K = _randn((2, 2, 16, 64), 1, torch.bfloat16)
+    cache = steps.TokenCache(K, K.clone())
+    q, k, v = (_randn((2, n, 64), n, torch.bfloat16) for n in (4, 2, 2))
+    dec = steps.SharedPrefixDecoder(cache, Hq=4, rotary=steps.Rotary(64) if turned else None)
+    before = {n: getattr(cache, n).clone() for n in ("K", "V", "weights", "positions", "lengths", "next_pos")}
+    off = torch.zeros(2 * 4 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(2, 4, 64)
+    bad = [(q.float(), k, v), (q[:, :3], k, v), (q, k.float(), v), (q, k, v[:1]), (q, k[:, :1], v), (q.cpu(), k, v)]
+    if not turned:  # (turned, the queries are copied)
+        bad += [(off, k, v), (q.transpose(0, 1).contiguous().transpose(0, 1), k, v)]
+    for args in bad:
+        with pytest.raises(csa.CsaError):
+            dec.step(*args)
+        torch.cuda.synchronize()
+        for n, x in before.items():
+            assert torch.equal(getattr(cache, n), x), n
+    dec.step(q, k, v)
+    assert cache.lengths.tolist() == [1, 1]
+
+
+def test_decoder_refuses_at_its_making(steps, csa):
+    """What no call of it could do."""
+    K = torch.zeros(2, 2, 64, 128, device="cuda", dtype=torch.bfloat16)
+    cache = steps.TokenCache(K, torch.zeros_like(K))
+    odd = torch.zeros(2, 2, 64, 129, device="cuda", dtype=torch.bfloat16)[..., :128]
+    for kw in (dict(Kp=K, Vp=K), dict(scale=0.0), dict(scale=math.inf), dict(decay=-0.5), dict(decay=math.nan),
+               dict(Kp=odd[:1], Vp=K[:1]), dict(Kp=K[:1], Vp=K[:1, :, :1].expand(1, 2, 64, 128))):
+        with pytest.raises(csa.CsaError):
+            steps.SharedPrefixDecoder(cache, Hq=8, **kw)
+    with pytest.raises(csa.CsaError):
+        steps.SharedPrefixDecoder(steps.TokenCache(odd, odd), Hq=8)
