@@ -726,9 +726,10 @@ typedef struct csa_cache_desc {
  * len[b] < budget, else over the unprotected slot of least weight (each head
  * its own; the lowest slot among equals).  The slot gets weight 0 and
  * position next_pos[b]; then len[b] (up to budget) and next_pos[b] advance by
- * one.  Needs n_sink + n_local < budget.  A length outside [0, budget], or no
- * unprotected slot (positions that are not distinct), records
- * CSA_ERR_DEVICE_INDEX and leaves that sequence's (that head's) slots alone.
+ * one.  Needs n_sink + n_local < budget.  A length outside [0, budget], a next_pos
+ * of 2^31 - 1 (the one behind it would read as inactive), or no unprotected slot
+ * (positions that are not distinct), records CSA_ERR_DEVICE_INDEX and leaves that
+ * sequence's (that head's) slots alone.
  * k and v must not overlap K or V (refused).
  * Calls that share a cache or its counters must not overlap on the GPU. */
 CSA_API csa_status csa_cache_insert(const csa_cache_desc* c, const void* k,

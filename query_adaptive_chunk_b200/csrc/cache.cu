@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
     sh_len = n;
     sh_next = at;
     __threadfence();
-    if (at >= 0 && n >= 0 && n <= c.budget) arrived = atomicAdd(c.counters + b, 1);
+    if (at >= 0 && at < INT_MAX && n >= 0 && n <= c.budget) arrived = atomicAdd(c.counters + b, 1);
   }
   load(tid);  // most often the cache is full: its slots' loads go out beside the length's
   // and so do the new row's: K by the first 64 threads, V by the next, 16 bytes each
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kInsThreads) cache_insert_kernel(
   __syncthreads();
   const int len = sh_len, next = sh_next;
   if (next < 0) return;  // an inactive sequence: left alone
-  if (len < 0 || len > c.budget) {
+  if (len < 0 || len > c.budget || next == INT_MAX) {  // (no position would follow)
     if (tid == 0) dev_flag(err, DEV_BAD_INDEX);
     return;
   }

@@ -375,3 +375,31 @@ def test_decoder_refuses_at_its_making(steps, csa):
             steps.SharedPrefixDecoder(cache, Hq=8, **kw)
     with pytest.raises(csa.CsaError):
         steps.SharedPrefixDecoder(steps.TokenCache(odd, odd), Hq=8)
+
+
+# ---------------------------------------------------------------- the last positions
+
+def test_insert_at_the_last_positions(steps, csa):
+    """2^31 - 2 is the last position that a token can take; at 2^31 - 1 the sequence is reported
+    and left alone, and does not turn into an inactive one."""
+    B, Hkv, T, D = 3, 2, 8, 64
+    K = _randn((B, Hkv, T, D), 1)
+    last = (1 << 31) - 2
+    cache = steps.TokenCache(K, K.clone(), lengths=_i32([T, 3, T]), next_pos=_i32([last, last + 1, 20]), n_local=2,
+                             positions=(torch.arange(T, dtype=torch.int32, device="cuda") + 5).expand(B, Hkv, T).contiguous())
+    k, v = _randn((B, Hkv, D), 2), _randn((B, Hkv, D), 3)
+    before = {n: getattr(cache, n).clone() for n in ("K", "V", "weights", "positions")}
+    cache.insert(k, v)
+    with pytest.raises(csa.CsaError) as e:
+        csa.csa_check_device_status()
+    assert e.value.status == 5
+    assert cache.next_pos.tolist() == [last + 1, last + 1, 21] and cache.lengths.tolist() == [T, 3, T]
+    for n, x in before.items():
+        assert torch.equal(getattr(cache, n)[1], x[1])
+    for b, at in ((0, last), (2, 20)):  # the lightest, the lowest of equals: slot 0
+        assert cache.positions[b, :, 0].tolist() == [at] * Hkv and torch.equal(cache.K[b, :, 0], k[b])
+    cache.insert(k, v)
+    with pytest.raises(csa.CsaError):
+        csa.csa_check_device_status()
+    assert cache.next_pos.tolist() == [last + 1, last + 1, 22]
+    assert not cache.counters.any()
