@@ -20,6 +20,7 @@
 #pragma once
 
 #include "internal.h"
+#include "prefix_split.h"
 
 namespace csa {
 
@@ -238,18 +239,9 @@ __device__ __forceinline__ PdPlace pd_locate(const PdShape& a, const PdShape& b,
   if (tid >> 5 < warps) {
     const int Wa = static_cast<int>(total >> 32), Wb = static_cast<int>(total & 0xffffffffu);
     // line a's CTAs: its share of the keys, at least one for each line with work
-    if (Wa > 0) {
-      const float ca = Wa * a.cost, cb = Wb * b.cost;
-      const int most = Wb == 0 ? b.ctas : b.ctas - 1;
-      const float share = Wb == 0 ? most : __fdividef(b.ctas * ca, ca + cb);
-      na = max(1, min(most, __float2int_rn(share)));
-      // units of one length: a whole number of CTAs each, so that none works on two
-      const int u = b.N == 1 ? units(a, 0) : 0;
-      if (u > 0 && na >= u) {
-        na = max(1, __float2int_rn(__fdividef(static_cast<float>(na), static_cast<float>(u)))) * u;
-        if (na > most) na -= u;
-      }
-    }
+    if (Wa > 0)
+      na = pd_line_a_ctas(Wa * a.cost, Wb * b.cost, b.ctas, b.N == 1 ? units(a, 0) : 0,
+                          a.lead * a.cost);
     if (tid == 0) ps->na = na;
     // each worker that takes part has a place
     const int Pa = max(1, min(na, Wa)), Pb = max(1, min((b.ctas - na) * b.workers, Wb));
