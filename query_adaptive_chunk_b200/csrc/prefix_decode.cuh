@@ -41,6 +41,7 @@ struct PdParams {
   float* lse_out;
   float* acc;
   float decay;
+  const int32_t* next_pos;  // [B] or null; negative: the sequence is inactive
 };
 
 // prefix_decode_bf16.cu

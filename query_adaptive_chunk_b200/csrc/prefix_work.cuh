@@ -52,18 +52,14 @@ struct PdShape {
   const int32_t* prefix_len;   // [N] or null: Tp
   const int32_t* group_start;  // [N + 1] or null: one group of all sequences
   const int32_t* len;          // [B] or null: T
-  const int32_t* next_pos;     // [B] or null; negative: the sequence is inactive, without keys
   DevErr err;
 };
 
 __device__ __forceinline__ int pd_prefix_len(const PdShape& s, int n) {
   return s.prefix_len ? pd_clamp(__ldg(s.prefix_len + n), s.Tp, s.err) : static_cast<int>(s.Tp);
 }
-__device__ __forceinline__ bool pd_active(const PdShape& s, int b) {
-  return s.next_pos == nullptr || __ldg(s.next_pos + b) >= 0;
-}
 __device__ __forceinline__ int pd_own_len(const PdShape& s, int b) {
-  if (s.T == 0 || !pd_active(s, b)) return 0;
+  if (s.T == 0) return 0;
   return s.len ? pd_clamp(__ldg(s.len + b), s.T, s.err) : static_cast<int>(s.T);
 }
 // Item i: prefix i, or the own cache of sequence i - N.  Its keys as they
@@ -71,8 +67,7 @@ __device__ __forceinline__ int pd_own_len(const PdShape& s, int b) {
 __device__ __forceinline__ int pd_raw_keys(const PdShape& s, int i) {
   if (i < s.N) return s.prefix_len ? __ldg(s.prefix_len + i) : static_cast<int>(s.Tp);
   if (s.T == 0) return 0;
-  const int n = s.len ? __ldg(s.len + i - s.N) : static_cast<int>(s.T);
-  return pd_active(s, i - s.N) ? n : 0;
+  return s.len ? __ldg(s.len + i - s.N) : static_cast<int>(s.T);
 }
 __device__ __forceinline__ int pd_item_keys(const PdShape& s, int i) {
   return i < s.N ? pd_prefix_len(s, i) : pd_own_len(s, i - s.N);
