@@ -117,9 +117,17 @@ def _p(x):
     return ctypes.c_void_p(int(x))
 
 
+# torch.cuda.current_stream().cuda_stream without its 3 us of wrapping, in a torch that
+# has these two (they are not public)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _s(stream):
-    if stream is None:  # torch.cuda.current_stream().cuda_stream, without its 3 us of wrapping
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    if stream is None:
+        if _raw_stream is None or _device is None:
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(_raw_stream(_device()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))

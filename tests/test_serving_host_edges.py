@@ -164,3 +164,15 @@ def test_strides_of_single_entries_are_not_used(csa):
             d.k_stride = (ctypes.c_int64 * 3)(64 * 128, 1, 128)
         assert csa.lib.csa_prefix_decode(ctypes.byref(d), None) in (INVALID, UNSUPPORTED)
         assert word in csa.csa_last_error_string(), change
+
+
+@pytest.mark.parametrize("missing", ["_raw_stream", "_device"])
+def test_current_stream_by_torchs_public_call(csa, monkeypatch, missing):
+    """A torch without the two short cuts still gives the current stream."""
+    import types
+
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=0x1230))
+    monkeypatch.setattr(csa, missing, None)
+    assert csa._s(None).value == 0x1230
+    assert csa._s(0x77).value == 0x77
