@@ -650,8 +650,10 @@ CSA_API csa_status csa_rotary_table(int rot, double theta, int scaling, double f
  *   (a, c) = (i, i + rot/2) for CSA_ROTARY_HALF, (2i, 2i + 1) for
  *   CSA_ROTARY_INTERLEAVED, A = amplitude;
  * values from rot on are copied.  transpose != 0 turns by -t (same A): the
- * gradient of x from that of y.  The angle is p w_i modulo one turn in 64-bit
- * integers, so far positions keep their accuracy; sums are fp32.
+ * gradient of x from that of y.  The angle is p times the table's entry modulo
+ * one turn in 64-bit integers, exact at far positions too; the table's entries are
+ * fp64 values of w_i / 2 pi (2^-22 turns at p = 2^31 at most, for the formulas' w_i
+ * <= 1); sums are fp32.
  *   x, y [B, S, H, D] of `dtype` by strides in elements (batch, token, head;
  *   the last index dense).  y == x with equal strides turns in place; other
  *   overlaps, of an output with an input, with the other output or among its

@@ -26,9 +26,11 @@ struct Launch {
 };
 
 // A launch that may start while the kernel before it on the stream drains
-// (programmatic dependent launch): the kernel waits for that one with
-// pdl_wait() before it touches memory, and lets the next one in with
-// pdl_next().
+// (programmatic dependent launch): before pdl_wait() the kernel must read nothing
+// that the one before it writes, and write nothing that it reads.  What still
+// earlier kernels wrote may be read ahead of the wait only where the kernel
+// before it is an ordinary launch, which waited for them.  pdl_next() lets the
+// next one in.
 template <typename... Params, typename... Args>
 cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
                           cudaStream_t stream, Args... args) {

@@ -360,6 +360,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) merge_kernel(const PdParams 
   float* acc = p.acc ? p.acc + static_cast<int64_t>(u) * s.T : nullptr;
   const float* lg = p.logits + static_cast<int64_t>(u) * s.G * p.Tl;
   const int64_t k1 = min(k0 + share, static_cast<int64_t>(len)), j_first = k0 + 4 * tid;
+  // (the lengths, next_pos and the sums are earlier kernels': the attention kernel is an
+  // ordinary launch that waited for them, and writes none of them)
   float old_first[4] = {0.f, 0.f, 0.f, 0.f};
   if (acc != nullptr && p.decay != 0.f)
 #pragma unroll
@@ -659,6 +661,7 @@ cudaError_t launch_attend_f32(const Launch& l, const PdParams& p) {
   cudaError_t e = cudaFuncSetAttribute(attend_f32_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  // an ordinary launch: the merge behind it reads what earlier kernels wrote
   attend_f32_kernel<D><<<p.b.s.ctas, kF32Workers * kF32Threads, smem, l.stream>>>(p);
   return cudaGetLastError();
 }

@@ -85,6 +85,7 @@ cudaError_t launch(const Launch& l, const PdParams& p, std::string* why) {
   cudaError_t e = cudaFuncSetAttribute(attend_bf16_kernel<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  // an ordinary launch: the merge behind it reads what earlier kernels wrote
   attend_bf16_kernel<D, NT><<<s.ctas, kTcThreads, smem, l.stream>>>(k, v, q, qs, o, m, p);
   return cudaGetLastError();
 }

@@ -15,9 +15,11 @@
 // The logits of own keys go to memory (4 bytes a row and key) for the merge.
 //
 // Bound by HBM: a step is 64 D bytes of K and V against about 60
-// instructions; with 192 KB in flight per SM the loads run ahead of the
-// products (32 sequences over 8K tokens, 67 MB here beside 34 MB of line a: 5.5
-// TB/s of both from the first row's arrival to the last).  Rows past a unit's keys are filled with zeros by the copy itself,
+// instructions; with all stages of a ring but one on their way while a warp waits
+// (128 KB per SM at D = 128, 160 KB at D = 64) the loads run ahead of the products (32
+// sequences over 8K tokens, 67 MB here beside 34 MB of line a, on one set of
+// inputs and so partly from L2: 5.5 TB/s of both from the first row's arrival to the
+// last).  Rows past a unit's keys are filled with zeros by the copy itself,
 // so what the cache holds there never enters a product.
 #pragma once
 

@@ -8,10 +8,13 @@
 //
 // Angles.  cos and sin only need p w_i modulo one turn, so a frequency is
 // held as the 64-bit fraction of a turn per position (w / 2 pi * 2^64) and
-// p w_i is one integer product that wraps by itself: exact modulo a turn
-// for any 32-bit position (also a negative one), 2^-33 turns of error at
-// p = 2^31 from the table's rounding.  The top 32 bits, as a float in
-// [-1, 1) half turns, go to sincospif: no range reduction, no 64-bit float.
+// p w_i is one integer product that wraps by itself: the table's own frequency
+// turns exactly modulo a turn at any 32-bit position (also a negative one).
+// The table is formed in 64-bit floats, off by at most (|ln w| + 8) 2^-53 of w
+// (a negative own frequency by 2^-54 turns besides): at p = 2^31 an angle is
+// within 2^-22 turns of the formula's, 2^-24.3 measured for theta up to 10^8.  The
+// top 32 bits, as a float in [-1, 1) half turns, go to sincospif: no range
+// reduction, no 64-bit float.
 //
 // Bound by HBM: 2 * bytes(q, k).  A thread keeps the sines and cosines of
 // its V pairs in registers and runs over the heads (stride J), so a token's

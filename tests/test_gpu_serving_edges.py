@@ -403,3 +403,79 @@ def test_insert_at_the_last_positions(steps, csa):
         csa.csa_check_device_status()
     assert cache.next_pos.tolist() == [last + 1, last + 1, 22]
     assert not cache.counters.any()
+
+
+# ---------------------------------------------------------------- the frequency table
+
+def _two_pi():
+    """2 pi to 60 digits, by Machin's formula."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 70
+
+    def arctan_inv(n):
+        total, term, k = Decimal(0), Decimal(1) / n, 0
+        while abs(term) > Decimal(10) ** -68:
+            total += term / (2 * k + 1) * (-1) ** k
+            term, k = term / (n * n), k + 1
+        return total
+    return 8 * (4 * arctan_inv(5) - arctan_inv(239))
+
+
+def _table(r):
+    return [x % (1 << 64) for x in r.table.tolist()]
+
+
+def _turns_off(table, exact):
+    """Distance of a table's entries from exact turns per position, modulo one."""
+    from decimal import Decimal
+    off = []
+    for got, t in zip(table, exact):
+        d = (Decimal(got) / (1 << 64) - t) % 1
+        off.append(float(min(abs(d), abs(1 - abs(d)))))
+    return off
+
+
+@pytest.mark.parametrize("rot,theta", [(128, 10000.0), (128, 500000.0), (64, 1000000.0), (2, 10000.0), (512, 1e8)])
+def test_rotary_table_is_good_to_64_bit_floats(steps, rot, theta):
+    """w = theta^(-2i/rot) in 64-bit floats: the exponent's rounding is |ln w| 2^-53 of
+    w, pow at most two steps of 2^-52, 2 pi, the division and the exponent's own products 2^-53
+    each: (|ln w| + 8) 2^-53 of w / 2 pi, and 2^-64 of the entry's last place."""
+    from decimal import Decimal
+    tau = _two_pi()
+    r = steps.Rotary(rot, theta=theta)
+    w = [Decimal(theta) ** (Decimal(-2 * i) / rot) for i in range(rot // 2)]
+    off = _turns_off(_table(r), [x / tau for x in w])
+    for i, (x, d) in enumerate(zip(w, off)):
+        assert d <= (abs(math.log(float(x))) + 8) * 2.0 ** -53 * float(x / tau) + 2.0 ** -64, i
+    print("largest error in turns at position 2^31: 2^%.1f" % math.log2(max(off) * 2.0 ** 31))
+
+
+def test_rotary_table_of_own_frequencies(steps):
+    """2 pi and the division, 2^-53 each of the whole number of turns; a negative frequency's
+    turns are taken from one, 2^-54."""
+    from decimal import Decimal
+    tau = _two_pi()
+    w = torch.cat([torch.rand(100, dtype=torch.float64) * 20 - 10, torch.rand(28, dtype=torch.float64) * 1e-6,
+                   torch.tensor([-1e-9, 0.0, 6.0, -6.5], dtype=torch.float64)])
+    r = steps.Rotary(2 * len(w), freqs=w.cuda())
+    exact = [Decimal(x) / tau for x in w.tolist()]
+    for x, d in zip(exact, _turns_off(_table(r), exact)):
+        assert d <= 2 * 2.0 ** -53 * abs(float(x)) + (2.0 ** -54 if x < 0 else 0.0) + 2.0 ** -64
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_angles_wrap_exactly(steps, layout):
+    """Position times table entry modulo a turn is exact: the result is that of the
+    table's own frequency, at any 32-bit position."""
+    rot = 128
+    r = steps.Rotary(rot, theta=500000.0, layout=layout)
+    pos = [0, 1, 131071, (1 << 31) - 1, (1 << 31) - 2, 1431655765, -1, -(1 << 31)]
+    x = _randn((1, len(pos), 1, rot), 5)
+    y = to_np(r.rotate(x, positions=_i32([pos])))[0, :, 0]
+    xs = to_np(x)[0, :, 0]
+    t = np.array([[(p * e) % (1 << 64) / 2.0 ** 64 for e in _table(r)] for p in pos]) * 2 * math.pi
+    a, b = (xs[:, :64], xs[:, 64:]) if layout == "half" else (xs[:, ::2], xs[:, 1::2])
+    u, v = a * np.cos(t) - b * np.sin(t), b * np.cos(t) + a * np.sin(t)
+    got = (y[:, :64], y[:, 64:]) if layout == "half" else (y[:, ::2], y[:, 1::2])
+    for g, want in zip(got, (u, v)):
+        assert np.all(np.abs(g - want) <= 6e-7 * (np.abs(a) + np.abs(b)) + U32 * np.abs(want))
