@@ -571,15 +571,13 @@ class SharedPrefixDecoder:
             weights=cache.weights if accumulate else None, decay=decay, workspace=self.workspace,
             workspace_bytes=nbytes, next_pos=cache.next_pos, **kw)
 
-    def _check_q(self, q):
-        _dense("q", q, self.cache.K.dtype, self.out.shape)
-        if q.device != self.out.device or q.data_ptr() % 16:
-            _bad(f"q must be on {self.out.device} and start on 16 bytes")
-
     def attend(self, q: torch.Tensor, stream=None):
         """Attention of q [B, Hq, D] over the prefixes and the cache as they
         are; returns (out, lse), this decoder's buffers."""
-        self._check_q(q)
+        _dense("q", q, self.cache.K.dtype, self.out.shape)
+        return self._attend(q, stream)
+
+    def _attend(self, q, stream):
         self.desc.q = q.data_ptr()
         csa.csa_prefix_decode(self.desc, stream=stream)
         return self.out, self.lse
@@ -593,6 +591,9 @@ class SharedPrefixDecoder:
             self.rotary.rotate(q.detach()[:, None], k.detach()[:, None], positions=c.next_pos[:, None],
                                q_out=self.q[:, None], k_out=self.k[:, None], stream=stream)
             q, k = self.q, self.k
-        self._check_q(q)  # before the cache changes
+        # before the cache changes
+        _dense("q", q, c.K.dtype, self.out.shape)
+        if q.device != self.out.device or q.data_ptr() % 16:
+            _bad(f"q must be on {self.out.device} and start on 16 bytes")
         c.insert(k, v, stream=stream)
-        return self.attend(q, stream=stream)
+        return self._attend(q, stream)
