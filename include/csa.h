@@ -820,7 +820,7 @@ typedef struct csa_prefix_decode_desc {
   float decay;
   void* workspace;
   int64_t workspace_bytes;
-  const int32_t* next_pos; /* NULL (all active) or [B] */
+  const int32_t* next_pos; /* NULL (all active) or [B], 4-byte aligned */
 } csa_prefix_decode_desc;
 
 /* `weights`: whether the calls add up weights.  < 0 on sizes csa_prefix_decode

@@ -1590,7 +1590,7 @@ csa_status csa_prefix_decode(const csa_prefix_decode_desc* d, csa_stream stream)
   CSA_TRY(check_ptr(d->prefix_len, "prefix_len", false));
   CSA_TRY(check_ptr(d->group_start, "group_start", false));
   CSA_TRY(check_ptr(d->len, "len", false));
-  CSA_TRY(check_ptr(d->next_pos, "next_pos", false));
+  CSA_TRY(check_ptr(d->next_pos, "next_pos", false, 4));
   CSA_TRY(check_ptr(d->lse_out, "lse_out", false));
   CSA_TRY(check_ptr(d->weights, "weights", false));
   CSA_TRY(check_ptr(d->workspace, "workspace"));

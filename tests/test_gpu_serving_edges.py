@@ -103,7 +103,7 @@ def test_step_leaves_a_paused_sequence_alone(steps, csa, dtype, G, prefixes):
 def test_attend_takes_a_paused_batch(steps, csa):
     """Every sequence paused: nothing but zeros and -inf, the sums as they were."""
     K = _randn((3, 2, 40, 128), 1, torch.bfloat16)
-    cache = steps.TokenCache(K, K.clone(), lengths=_i32([40, 3, 0]), next_pos=_i32([-1, -2, -(1 << 31)]),
+    cache = steps.TokenCache(K, K.clone(), lengths=_i32([40, 3, 0]), next_pos=_i32([0, -1, -2, -(1 << 31)])[1:],
                              weights=_randn((3, 2, 40), 2))
     before = cache.weights.clone()
     Kp = _randn((1, 2, 300, 128), 3, torch.bfloat16)
