@@ -22,8 +22,8 @@
 // 23 bytes a clock, 1430 clocks a chunk at D = 128, against 640 clocks of
 // products (QK^T at N = 64 is bound by its shared-memory operands) and 512 of
 // exponentials per half: up to 128 rows memory is the bound (128K tokens, 8 KV
-// heads, 128 rows: 95 us, 87% of the copy rate).  With 256 rows a chunk takes
-// about 2000 clocks (151 us): the tensor pipe passes between the four groups of
+// heads, 128 rows: this kernel 95 us, 87% of the copy rate, 1310 clocks a chunk).  With
+// 256 rows a chunk takes about 2000 clocks (146 us): the tensor pipe passes between the four groups of
 // products per chunk (QK^T and PV of each half), each short.  Measured there
 // and not kept: half or a quarter of the exponentials on the FMA pipe (8% and 6%
 // slower), four softmax warps per scheduler instead of two, a column half each
@@ -373,7 +373,8 @@ __device__ __forceinline__ void attend_tc(const CUtensorMap& tmK, const CUtensor
     bool ok = true;
     // In a unit of both halves the two warps of a scheduler take turns at the
     // exponentials (half 0 first): in step they share the special-function unit
-    // there and leave it idle elsewhere (158 against 151 us as above).
+    // there and leave it idle elsewhere (158 against 151 us, measured
+    // in turn).
     auto turn_wait = [&]() -> bool {
       const uint32_t n = turns++;
       return warp_wait(turn + 8 * (4 * hf + wr), hf ? n & 1u : (n & 1u) ^ 1u, shape.err);
