@@ -588,7 +588,8 @@ class SharedPrefixDecoder:
         For serving: no gradient is kept."""
         c = self.cache
         if self.rotary is not None:
-            self.rotary.rotate(q.detach()[:, None], k.detach()[:, None], positions=c.next_pos[:, None],
+            q, k = (x.detach() if x.requires_grad else x for x in (q, k))
+            self.rotary.rotate(q[:, None], k[:, None], positions=c.next_pos[:, None],
                                q_out=self.q[:, None], k_out=self.k[:, None], stream=stream)
             q, k = self.q, self.k
         # before the cache changes
